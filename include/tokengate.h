@@ -18,7 +18,9 @@
  * Further calls serve the layers around it: budget sweeps and random-K selection,
  * the backward of the gated attention (gradients of the log-gates, gains and
  * temperatures), the element-wise steps of a stack of gated upper layers that
- * emits a compacted KV cache, and a Gated DeltaNet layer over the kept rows.
+ * emits a compacted KV cache, a Gated DeltaNet layer over the kept rows, and
+ * decoding from what the prefill leaves: attention over a paged cache, the cache's
+ * pages, a step of the delta rule and a beam search's selection.
  *
  * Conventions shared by every call
  *   - Device pointers point to memory on the current CUDA device; "host" arrays
@@ -107,7 +109,8 @@ TG_API tg_status tg_device_status(tg_stream_t stream, uint32_t* bits_out);
  * up (forward or backward), 4 the top-K selection produced more rows than M_b (extra rows skipped),
  * 8 a kept index outside the prompt batch reached the gather (row skipped),
  * 16 a gather pipeline wait gave up, 32 a chunk load of the chunked delta-rule
- * scan did not land.
+ * scan did not land, 64 a page, length or parent outside its range reached a
+ * decoding call (skipped).
  */
 TG_API tg_status tg_last_device_error(tg_stream_t stream, int32_t* code_out);
 
@@ -520,6 +523,192 @@ TG_API tg_status tg_delta_scan_workspace_bytes(int32_t batch, const int32_t* cu_
 /* Workspace bytes tg_gated_attention_backward needs for this batch (host-only). */
 TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int32_t* cu_kept_h,
                                                        int32_t n_q_heads, size_t* bytes_out);
+
+/*
+ * Decoding after the gated prefill.  The layers above the gate keep KV only for
+ * the kept rows, so a decoding step attends to few keys, but with the same bias:
+ * the log-gates stay in the cache beside k and v (0 for question and generated
+ * tokens).  The calls below read and grow that cache one token at a time, for
+ * single sequences and for the beams of a search.
+ *
+ * A paged cache is a pool of n_pages pages of page_size tokens (16, 32, 64 or
+ * 128) that its sequences share:
+ *   k_pages, v_pages  [n_pages, n_kv_heads, page_size, head_dim] per layer
+ *   logsig_pages      [n_pages, page_size] fp32, one for all layers
+ *   table             [batch, max_pages] int32: token j of sequence b lies in page
+ *                     table[b, j / page_size] at j % page_size
+ *   lens              [batch] int32 tokens per sequence
+ *   refs              [n_pages] int32: how many table entries hold a page; 0 = free
+ * All of it is device memory that the host never has to read, so a step can be
+ * captured in a CUDA graph.  The host cannot check what lies there; a kernel
+ * that meets a length outside [0, max_pages * page_size] (taken as the nearest
+ * bound), a page or a parent outside its range (skipped) sets bit 64 of the
+ * device status word.  Table entries behind a sequence's last page are neither
+ * read nor written.  At most TG_MAX_SEQS sequences per call.
+ */
+#define TG_MAX_SEQS 1024
+
+/*
+ * tg_paged_attention: step 4 for one new token per sequence, over the cache.
+ * For sequence b, head h, with the n = lens[b] cached tokens:
+ *     logit_j = (q_b . k_j) / (sqrt(head_dim) * temp[h]) + gain[h] * logsig[j]
+ *     out_b = sum_{j < n} softmax_j(logit) v_j,   lse[h, b] = log sum_j exp(logit_j)
+ * The new token's own k and v are in the cache already (tg_cache_append).  A
+ * token whose log-gate is -inf has no weight, whatever the gain and its k and v;
+ * a sequence that no token is left of (n = 0 among them) gets out = 0 and
+ * lse = -inf.
+ *   q     device [batch, n_q_heads, head_dim];  out the same shape and dtype
+ *   logsig_pages may be NULL (no bias); gain, temp device [n_q_heads] fp32
+ *   lse   device [n_q_heads, batch] fp32 or NULL
+ *   workspace, workspace_bytes
+ *         device scratch of tg_paged_attention_workspace_bytes, or NULL.  With it
+ *         the keys of a sequence are split over several SMs and joined in a fixed
+ *         order; without it one SM reads them all.  16-byte aligned; zeroed once
+ *         by the caller after allocating it, every call leaves its counters
+ *         zero again.  TG_ERR_WORKSPACE when smaller.  Calls that share a
+ *         workspace must not overlap on the GPU.
+ *   head_dim 64 or 128, 16-byte aligned q, k_pages, v_pages and out.
+ */
+TG_API tg_status tg_paged_attention(const void* q, const void* k_pages, const void* v_pages,
+                                    tg_dtype dtype, int32_t batch, int32_t n_q_heads,
+                                    int32_t n_kv_heads, int32_t head_dim, int32_t n_pages,
+                                    int32_t page_size, const int32_t* table, int32_t max_pages,
+                                    const int32_t* lens, const float* logsig_pages,
+                                    const float* gain, const float* temp, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, tg_stream_t stream);
+
+/* Workspace bytes tg_paged_attention can use on the current device (host-only). */
+TG_API tg_status tg_paged_attention_workspace_bytes(tg_dtype dtype, int32_t batch,
+                                                    int32_t n_q_heads, int32_t n_kv_heads,
+                                                    int32_t head_dim, size_t* bytes_out);
+
+/*
+ * tg_cache_update: one step of a paged cache's tables: fork, free and growth.
+ *   1. Output sequence i takes the pages and the length of input sequence
+ *      parent[i] (-1: none, it starts empty); parent == NULL: its own
+ *      (batch_out == batch_in).  Every count follows: a page that an input
+ *      sequence with c children held once is now held c times, so the pages
+ *      that no output sequence holds become free.
+ *   2. It grows by n_i = cu_new[i + 1] - cu_new[i] tokens (cu_new == NULL: none).
+ *      When n_i > 0, its last page is partly filled and held by others too, a
+ *      free page takes its place: copy_src[i], copy_dst[i] name the pair that
+ *      tg_cache_copy_pages then copies.  Of the growing sequences that hold one
+ *      page the last, when nobody else holds it, keeps it.  Free pages are
+ *      handed out lowest number first, in the order of the sequences.
+ *      A sequence that does not fit into max_pages does not grow.  When the
+ *      free pages run out, the first sequence that lacks one does not grow, nor
+ *      does any after it that needs a page or shares the one it would write to.
+ *      start[i] is the position of its first new token (its length before), or
+ *      -1 when it did not grow; lens_out[i] counts the new tokens.
+ *   table_in [batch_in, max_pages], lens_in [batch_in], refs_in [n_pages]
+ *   table_out [batch_out, max_pages], lens_out, start, copy_src, copy_dst
+ *   [batch_out], refs_out [n_pages].  copy_src and copy_dst are -1 where nothing
+ *   is copied.  refs_out may be refs_in; with parent == NULL table_out may be
+ *   table_in and lens_out may be lens_in.  No other buffers may overlap.
+ */
+TG_API tg_status tg_cache_update(const int32_t* table_in, const int32_t* lens_in, int32_t batch_in,
+                                 const int32_t* refs_in, int32_t n_pages, int32_t page_size,
+                                 int32_t max_pages, const int32_t* parent, int32_t batch_out,
+                                 const int32_t* cu_new, int32_t* table_out, int32_t* lens_out,
+                                 int32_t* refs_out, int32_t* start, int32_t* copy_src,
+                                 int32_t* copy_dst, tg_stream_t stream);
+
+/*
+ * tg_cache_compact: moves the live pages (refs > 0) into the lowest page numbers,
+ * so that the rest of the pool can be given back.  With n live pages, the i-th
+ * live page numbered n or above goes to the i-th free page below n; the others
+ * stay.
+ *   page_map [n_pages]   new number of every live page, -1 for free ones
+ *   table_out, refs_out  renumbered (each may be its input; no other overlap)
+ *   copy_src, copy_dst   [n_pages] the moves for tg_cache_copy_pages, -1 behind them
+ *   counts [2]           n, and how many pages move
+ */
+TG_API tg_status tg_cache_compact(const int32_t* table_in, const int32_t* lens, int32_t batch,
+                                  const int32_t* refs_in, int32_t n_pages, int32_t page_size,
+                                  int32_t max_pages, int32_t* table_out, int32_t* refs_out,
+                                  int32_t* page_map, int32_t* copy_src, int32_t* copy_dst,
+                                  int32_t* counts, tg_stream_t stream);
+
+/* One pool whose pages are copied: `layers` arrays of n_pages pages, one after another. */
+typedef struct {
+    void* base;          /* device [layers, n_pages, page_bytes], 16-byte aligned */
+    int64_t page_bytes;  /* a multiple of 16 */
+    int32_t layers;
+} tg_page_pool;
+
+/*
+ * tg_cache_copy_pages: in every layer of every pool, page copy_src[i] is copied to
+ * page copy_dst[i], for i < n_copies (i < min(n_copies, *count) with a count in
+ * device memory).  Pairs with a negative or equal numbers are skipped.  No page
+ * may be the destination of two pairs, nor both a destination and a source.
+ *   pools  host array of n_pools (<= TG_MAX_GATHER_TENSORS) entries
+ */
+TG_API tg_status tg_cache_copy_pages(const tg_page_pool* pools, int32_t n_pools, int32_t n_pages,
+                                     const int32_t* copy_src, const int32_t* copy_dst,
+                                     int32_t n_copies, const int32_t* count, tg_stream_t stream);
+
+/*
+ * tg_cache_append: writes new rows into their sequences' pages: row i of sequence
+ * b, cu_new[b] <= i < cu_new[b + 1], becomes token start[b] + i - cu_new[b].  The
+ * rows of a sequence with start[b] < 0 are skipped.
+ *   k, v      device [rows, n_kv_heads, head_dim];  logsig device [rows] fp32, or
+ *             NULL for 0 (a generated token); logsig_pages NULL: no log-gates
+ *   cu_new    device [batch + 1], start device [batch] (of tg_cache_update)
+ *   head_dim * element size a multiple of 16 bytes, 16-byte aligned k, v and pages.
+ */
+TG_API tg_status tg_cache_append(const void* k, const void* v, const float* logsig, tg_dtype dtype,
+                                 int64_t rows, int32_t batch, const int32_t* cu_new,
+                                 const int32_t* start, int32_t n_kv_heads, int32_t head_dim,
+                                 int32_t n_pages, int32_t page_size, const int32_t* table,
+                                 int32_t max_pages, void* k_pages, void* v_pages,
+                                 float* logsig_pages, tg_stream_t stream);
+
+/*
+ * tg_gated_delta_step: tg_gated_delta_scan for one new token per sequence, from
+ * the state that the scan or the last step left:
+ *     S'    = alpha S + beta (v - alpha S k^) k^^T,   out = S' q^
+ * with S = state_in[parent[b], h] (parent == NULL: state_in[b, h]; -1: zero), so
+ * the states of a beam search are reordered by the step's own read.
+ *   q, k, v, out [batch, n_heads, head_dim];  log_alpha, beta [batch, n_heads] fp32
+ *   state_in  [n_states, n_heads, head_dim (v), head_dim (k)] fp32
+ *   state_out [batch, n_heads, head_dim, head_dim] fp32; may be state_in when
+ *             parent is NULL, may not overlap it otherwise
+ *   head_dim 64 or 128; q, k, v, state_in, state_out 16-byte aligned.
+ */
+TG_API tg_status tg_gated_delta_step(const void* q, const void* k, const void* v, tg_dtype dtype,
+                                     const float* log_alpha, const float* beta, int32_t batch,
+                                     int32_t n_heads, int32_t head_dim, float eps,
+                                     const float* state_in, int32_t n_states,
+                                     const int32_t* parent, float* state_out, void* out,
+                                     tg_stream_t stream);
+
+#define TG_MAX_BEAMS 32
+
+/*
+ * tg_beam_select: the n_out best continuations of each group of beams.  Beam b of
+ * group g continues with token t at the score
+ *     scores[g, b] + logits[r, t] - log sum_u exp(logits[r, u]),   r = g * beams + b
+ * computed in 64 bits from the logits' exponentials summed in 32; larger first,
+ * equal ones by lower b * vocab + t.  Only finite scores are candidates: a token
+ * of logit -inf, a beam of score -inf, and a beam whose logits hold NaN or +inf
+ * offer none.
+ *   logits  device [n_groups * beams, vocab], 16-byte aligned;  scores [n_groups, beams] fp32
+ *   scores_out [n_groups, n_out] fp32 in order, parent_out int32 the row r (the
+ *   parent of tg_cache_update and tg_gated_delta_step), token_out int32; places
+ *   that no candidate is left for get -inf, -1, -1.
+ *   beams 1 .. TG_MAX_BEAMS, n_out 1 .. 2 * TG_MAX_BEAMS, vocab <= 2^20.
+ *   workspace  device scratch of tg_beam_select_workspace_bytes, 16-byte aligned
+ *              (TG_ERR_WORKSPACE when smaller); calls that share it must not
+ *              overlap on the GPU.
+ */
+TG_API tg_status tg_beam_select(const void* logits, tg_dtype dtype, const float* scores,
+                                int32_t n_groups, int32_t beams, int32_t vocab, int32_t n_out,
+                                float* scores_out, int32_t* parent_out, int32_t* token_out,
+                                void* workspace, size_t workspace_bytes, tg_stream_t stream);
+
+/* Workspace bytes tg_beam_select needs (host-only). */
+TG_API tg_status tg_beam_select_workspace_bytes(int32_t n_groups, int32_t beams, int32_t vocab,
+                                                int32_t n_out, size_t* bytes_out);
 
 #ifdef __cplusplus
 }

@@ -10,10 +10,14 @@ news write-ups, "how it works"):
 
     gate_score -> topk_select -> compact_gather -> gated_attention
 
-``gated_prefill`` chains them for one prompt batch.
+``gated_prefill`` chains them for one prompt batch.  Decoding from what a prefill
+leaves goes through ``paged_attention``, the ``cache_*`` calls, ``gated_delta_step``
+and ``beam_select`` (``pipeline.PagedCache`` and ``pipeline.GatedDecoder`` put them
+together).
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -27,6 +31,8 @@ __all__ = [
     "attention_kernel", "topk_select_multi", "random_select", "gated_attention_backward",
     "attention_backward_workspace_bytes", "rmsnorm", "qkv_rope_emit", "swiglu", "gated_delta_scan",
     "topk_workspace_bytes", "topk_workspace", "delta_scan_workspace_bytes",
+    "paged_attention", "paged_attention_workspace", "cache_update", "cache_compact",
+    "cache_copy_pages", "cache_append", "gated_delta_step", "beam_select", "beam_select_workspace",
 ]
 
 TG_BF16, TG_FP32 = 0, 1
@@ -46,8 +52,14 @@ EXPORTED_SYMBOLS = (
     "tg_qkv_rope_emit", "tg_swiglu", "tg_gated_delta_scan", "tg_last_device_error",
     "tg_topk_workspace_bytes", "tg_gate_score_hist", "tg_topk_select_ws",
     "tg_gated_delta_scan_chunked", "tg_delta_scan_workspace_bytes", "tg_topk_select_multi_ws",
+    "tg_paged_attention", "tg_paged_attention_workspace_bytes", "tg_cache_update",
+    "tg_cache_compact", "tg_cache_copy_pages", "tg_cache_append", "tg_gated_delta_step",
+    "tg_beam_select", "tg_beam_select_workspace_bytes",
 )
 MAX_BUDGETS = 8
+MAX_SEQS = 1024
+MAX_BEAMS = 32
+PAGE_SIZES = (16, 32, 64, 128)
 ATTN_KERNELS = {0: "attn_simt_kernel", 1: "attn_tc_kernel", 2: "attn_tc_kernel (key-range split)",
                 3: "attn_pair_kernel"}
 
@@ -64,6 +76,15 @@ class GatherTensor(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
                 ("row_elems", ctypes.c_int32), ("rope_heads", ctypes.c_int32)]
 
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64),
+                ("layers", ctypes.c_int32)]
+
+
+CacheUpdate = collections.namedtuple("CacheUpdate", "table lens refs start copy_src copy_dst")
+CacheCompact = collections.namedtuple("CacheCompact",
+                                      "table refs page_map copy_src copy_dst counts")
 
 _lib = None
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -128,6 +149,21 @@ def library():
                                               _vp]
     L.tg_delta_scan_workspace_bytes.argtypes = [_i32, _i32p, _i32, _i32,
                                                 ctypes.POINTER(ctypes.c_size_t)]
+    sz, szp = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    L.tg_paged_attention.argtypes = [_vp, _vp, _vp, ctypes.c_int] + [_i32] * 6 + [
+        _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+    L.tg_paged_attention_workspace_bytes.argtypes = [ctypes.c_int, _i32, _i32, _i32, _i32, szp]
+    L.tg_cache_update.argtypes = [_vp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32] + [_vp] * 8
+    L.tg_cache_compact.argtypes = [_vp, _vp, _i32, _vp, _i32, _i32, _i32] + [_vp] * 7
+    L.tg_cache_copy_pages.argtypes = [ctypes.POINTER(PagePool), _i32, _i32, _vp, _vp, _i32, _vp,
+                                      _vp]
+    L.tg_cache_append.argtypes = [_vp, _vp, _vp, ctypes.c_int, _i64, _i32, _vp, _vp, _i32, _i32,
+                                  _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp]
+    L.tg_gated_delta_step.argtypes = [_vp, _vp, _vp, ctypes.c_int, _vp, _vp, _i32, _i32, _i32,
+                                      _f32, _vp, _i32, _vp, _vp, _vp, _vp]
+    L.tg_beam_select.argtypes = [_vp, ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                 _vp, sz, _vp]
+    L.tg_beam_select_workspace_bytes.argtypes = [_i32, _i32, _i32, _i32, szp]
     for name in EXPORTED_SYMBOLS:
         if name not in ("tg_status_string", "tg_last_error_message", "tg_version",
                         "tg_topk_workspace_bytes"):
@@ -658,3 +694,282 @@ def gated_prefill(h, q, k, v, W1, b1, w2, b2, gain, temp, cu_seqlens, doc_begin,
                              want_lse=want_lse)
     return dict(z=z, kept_idx=kept_idx, cu_kept=cu_kept, cu_kept_host=cu_kept_host, h=h_c, q=q_c,
                 k=k_c, v=v_c, logsig=logsig, out=o, lse=lse)
+
+
+# ---- decoding ----------------------------------------------------------------------------------
+
+
+def _workspace(workspace, device):
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
+            workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+
+
+def _pools(k_pages, v_pages, logsig_pages):
+    """(n_pages, n_kv_heads, page_size, head_dim) of one layer's pages."""
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [n_pages, n_kv_heads, page_size, head_dim]")
+    P, Hkv, page, d = k_pages.shape
+    _expect("k_pages", k_pages, (P, Hkv, page, d), k_pages.dtype, k_pages.device)
+    _expect("v_pages", v_pages, (P, Hkv, page, d), k_pages.dtype, k_pages.device)
+    _expect("logsig_pages", logsig_pages, (P, page), torch.float32, k_pages.device)
+    return P, Hkv, page, d
+
+
+def _table(table, lens, device):
+    """(batch, max_pages) of a page table and its lengths."""
+    if table.dim() != 2:
+        raise ValueError("table must be [batch, max_pages]")
+    B, mp = table.shape
+    _expect("table", table, (B, mp), torch.int32, device)
+    _expect("lens", lens, (B,), torch.int32, device)
+    return B, mp
+
+
+def paged_attention_workspace(batch, n_q_heads, n_kv_heads, head_dim, dtype=torch.bfloat16,
+                              device=None):
+    """A zeroed workspace for paged_attention of this shape (uint8 device tensor): with it a
+    sequence's keys are split over several SMs.  Calls on it must not overlap on the GPU."""
+    device = torch.device(device or "cuda")
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(device):
+        _check("tg_paged_attention_workspace_bytes", library().tg_paged_attention_workspace_bytes(
+            TG_BF16 if dtype in ("bf16", torch.bfloat16) else TG_FP32, batch, n_q_heads,
+            n_kv_heads, head_dim, ctypes.byref(out)))
+        return torch.zeros(int(out.value), dtype=torch.uint8, device=device)
+
+
+def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=None, temp=None,
+                    out=None, lse=None, want_lse=False, workspace="auto"):
+    """Token-gated attention of one new token per sequence over a paged cache.
+
+    q [B, Hq, d]; k_pages, v_pages [P, Hkv, page, d]; table [B, max_pages] and lens [B] int32 on
+    the device; logsig_pages [P, page] or None (no bias); gain (None: 1), temp (None: 1) [Hq].
+    workspace: "auto" (allocate and zero one), None (no split), or paged_attention_workspace(...),
+    which a decoding loop keeps.  Returns (out [B, Hq, d], lse [Hq, B] or None)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [batch, heads, head_dim]")
+    B, Hq, dh = q.shape
+    _expect("q", q, (B, Hq, dh), q.dtype, q.device)
+    P, Hkv, page, d = _pools(k_pages, v_pages, logsig_pages)
+    if d != dh or k_pages.dtype != q.dtype or k_pages.device != q.device:
+        raise ValueError(f"k_pages: {tuple(k_pages.shape)} {k_pages.dtype} on {k_pages.device} "
+                         f"for q {tuple(q.shape)} {q.dtype} on {q.device}")
+    if Hkv <= 0 or Hq % Hkv != 0:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} kv heads")
+    Bt, mp = _table(table, lens, q.device)
+    if Bt != B:
+        raise ValueError(f"table: {Bt} sequences, q has {B}")
+    _expect("gain", gain, (Hq,), torch.float32, q.device)
+    _expect("temp", temp, (Hq,), torch.float32, q.device)
+    _expect("out", out, (B, Hq, dh), q.dtype, q.device)
+    _expect("lse", lse, (Hq, B), torch.float32, q.device)
+    if workspace is not None and not isinstance(workspace, str):
+        _workspace(workspace, q.device)
+    _need_cuda(q, k_pages, v_pages, table, lens)
+    with torch.cuda.device(q.device):
+        one = torch.ones(Hq, device=q.device) if gain is None or temp is None else None
+        gain = one if gain is None else gain
+        temp = one if temp is None else temp
+        out = torch.empty_like(q) if out is None else out
+        if want_lse and lse is None:
+            lse = torch.empty((Hq, B), dtype=torch.float32, device=q.device)
+        if isinstance(workspace, str):
+            workspace = paged_attention_workspace(B, Hq, Hkv, dh, q.dtype, q.device)
+        # a workspace of no bytes has no address: the call needs none of it
+        ws = None if workspace is None or workspace.numel() == 0 else workspace
+        _check("tg_paged_attention", library().tg_paged_attention(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), _dtype_code(q), B, Hq, Hkv, dh, P, page,
+            _ptr(table), mp, _ptr(lens), _ptr(logsig_pages), _ptr(gain), _ptr(temp), _ptr(out),
+            _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(), _stream(q.device)))
+    return out, lse
+
+
+def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_out=None,
+                 lens_out=None, refs_out=None, start=None, copy_src=None, copy_dst=None):
+    """One step of a paged cache's tables: sequence i takes the pages of sequence parent[i] (-1:
+    none; parent None: its own) and grows by cu_new[i + 1] - cu_new[i] tokens.
+
+    table [B, max_pages], lens [B], refs [P], parent [B'], cu_new [B' + 1]: int32 on the device.
+    Outputs that are not given are allocated (a new table is -1 behind its sequences' pages);
+    refs_out may be refs, and without parents table_out and lens_out may be table and lens.
+    Returns a CacheUpdate: table, lens, refs, start [B'] (position of the first new token, -1
+    where the sequence did not grow), and copy_src, copy_dst [B'], the page copies for
+    cache_copy_pages that have to run before anything is appended."""
+    dev = table.device
+    B, mp = _table(table, lens, dev)
+    P = refs.shape[0]
+    _expect("refs", refs, (P,), torch.int32, dev)
+    Bo = B if parent is None else parent.shape[0]
+    _expect("parent", parent, (Bo,), torch.int32, dev)
+    _expect("cu_new", cu_new, (Bo + 1,), torch.int32, dev)
+    _expect("table_out", table_out, (Bo, mp), torch.int32, dev)
+    _expect("refs_out", refs_out, (P,), torch.int32, dev)
+    for name, t in (("lens_out", lens_out), ("start", start), ("copy_src", copy_src),
+                    ("copy_dst", copy_dst)):
+        _expect(name, t, (Bo,), torch.int32, dev)
+    _need_cuda(table, lens, refs)
+    with torch.cuda.device(dev):
+        i32 = dict(dtype=torch.int32, device=dev)
+        table_out = torch.full((Bo, mp), -1, **i32) if table_out is None else table_out
+        refs_out = torch.empty(P, **i32) if refs_out is None else refs_out
+        small = [lens_out, start, copy_src, copy_dst]
+        if any(t is None for t in small):
+            fresh = torch.empty((4, Bo), **i32)  # one allocation for those that are not given
+            small = [fresh[i] if t is None else t for i, t in enumerate(small)]
+        lens_out, start, copy_src, copy_dst = small
+        _check("tg_cache_update", library().tg_cache_update(
+            _ptr(table), _ptr(lens), B, _ptr(refs), P, page_size, mp, _ptr(parent), Bo,
+            _ptr(cu_new), _ptr(table_out), _ptr(lens_out), _ptr(refs_out), _ptr(start),
+            _ptr(copy_src), _ptr(copy_dst), _stream(dev)))
+    return CacheUpdate(table_out, lens_out, refs_out, start, copy_src, copy_dst)
+
+
+def cache_compact(table, lens, refs, page_size, table_out=None, refs_out=None):
+    """Renumbers the live pages (refs > 0) of a pool into its lowest page numbers.
+
+    Returns a CacheCompact: table, refs (renumbered; table_out and refs_out may be table and
+    refs), page_map [P] (a live page's new number, -1 for free ones), copy_src and copy_dst [P]
+    (the moves, -1 behind them) and counts [2] = live pages, moves.  The moves are made by
+    cache_copy_pages(pools, copy_src, copy_dst, counts[1:])."""
+    dev = table.device
+    B, mp = _table(table, lens, dev)
+    P = refs.shape[0]
+    _expect("refs", refs, (P,), torch.int32, dev)
+    _expect("table_out", table_out, (B, mp), torch.int32, dev)
+    _expect("refs_out", refs_out, (P,), torch.int32, dev)
+    _need_cuda(table, lens, refs)
+    with torch.cuda.device(dev):
+        i32 = dict(dtype=torch.int32, device=dev)
+        table_out = torch.full((B, mp), -1, **i32) if table_out is None else table_out
+        refs_out = torch.empty(P, **i32) if refs_out is None else refs_out
+        page_map, src, dst = torch.empty((3, P), **i32)
+        counts = torch.empty(2, **i32)
+        _check("tg_cache_compact", library().tg_cache_compact(
+            _ptr(table), _ptr(lens), B, _ptr(refs), P, page_size, mp, _ptr(table_out),
+            _ptr(refs_out), _ptr(page_map), _ptr(src), _ptr(dst), _ptr(counts), _stream(dev)))
+    return CacheCompact(table_out, refs_out, page_map, src, dst, counts)
+
+
+def cache_copy_pages(pools, copy_src, copy_dst, count=None):
+    """Copies page copy_src[i] to page copy_dst[i] in every layer of every pool [layers, P, ...];
+    pairs with a negative number are skipped.  count: device int32 [1], how many pairs to look at
+    (None: all).  No page may be a destination twice, nor both a source and a destination."""
+    if len(pools) > MAX_GATHER_TENSORS:
+        raise ValueError("too many pools")
+    n = copy_src.shape[0]
+    dev = copy_src.device
+    _expect("copy_src", copy_src, (n,), torch.int32, dev)
+    _expect("copy_dst", copy_dst, (n,), torch.int32, dev)
+    _expect("count", count, (1,), torch.int32, dev)
+    if not pools:
+        return
+    P = pools[0].shape[1] if pools[0].dim() > 1 else -1
+    arr = (PagePool * len(pools))()
+    for i, t in enumerate(pools):
+        if t.dim() < 3 or t.shape[1] != P:
+            raise ValueError(f"pools[{i}]: shape {tuple(t.shape)}, expected [layers, {P}, ...]")
+        _expect(f"pools[{i}]", t, t.shape, t.dtype, dev)
+        arr[i].base = t.data_ptr()
+        arr[i].page_bytes = int(np.prod(t.shape[2:], dtype=np.int64)) * t.element_size()
+        arr[i].layers = t.shape[0]
+    _need_cuda(copy_src, *pools)
+    with torch.cuda.device(dev):
+        _check("tg_cache_copy_pages", library().tg_cache_copy_pages(
+            arr, len(pools), P, _ptr(copy_src), _ptr(copy_dst), n, _ptr(count), _stream(dev)))
+
+
+def cache_append(k, v, cu_new, start, table, k_pages, v_pages, logsig=None, logsig_pages=None):
+    """Writes rows of k, v [rows, Hkv, d] (and log-gates [rows]; None: 0) into their sequences'
+    pages: row i of sequence b (cu_new[b] <= i < cu_new[b + 1]) becomes token
+    start[b] + i - cu_new[b]; start[b] < 0 skips the sequence.  cu_new [B + 1], start [B],
+    table [B, max_pages]: int32 on the device."""
+    P, Hkv, page, d = _pools(k_pages, v_pages, logsig_pages)
+    dev = k_pages.device
+    rows = k.shape[0]
+    _expect("k", k, (rows, Hkv, d), k_pages.dtype, dev)
+    _expect("v", v, (rows, Hkv, d), k_pages.dtype, dev)
+    _expect("logsig", logsig, (rows,), torch.float32, dev)
+    if logsig is not None and logsig_pages is None:
+        raise ValueError("logsig without logsig_pages")
+    B, mp = _table(table, None, dev)
+    _expect("cu_new", cu_new, (B + 1,), torch.int32, dev)
+    _expect("start", start, (B,), torch.int32, dev)
+    _need_cuda(k, v, cu_new, start, table, k_pages)
+    with torch.cuda.device(dev):
+        _check("tg_cache_append", library().tg_cache_append(
+            _ptr(k), _ptr(v), _ptr(logsig), _dtype_code(k), rows, B, _ptr(cu_new), _ptr(start),
+            Hkv, d, P, page, _ptr(table), mp, _ptr(k_pages), _ptr(v_pages), _ptr(logsig_pages),
+            _stream(dev)))
+
+
+def gated_delta_step(q, k, v, log_alpha, beta, state, parent=None, eps=1e-6, out=None,
+                     state_out=None):
+    """One token of the gated delta rule per sequence, from the state that gated_delta_scan or the
+    last step left: q, k, v [B, H, d], log_alpha, beta [B, H] fp32, state [S, H, d, d] fp32.
+
+    parent [B] int32 on the device: sequence b starts from state[parent[b]] (-1: from zero), the
+    reordering of a beam search; state_out may then not be state.  Without parents sequence b
+    starts from state[b], and state_out=state updates in place.
+    Returns (out [B, H, d], state_out [B, H, d, d])."""
+    if q.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be [batch, heads, head_dim], state [n, heads, head_dim, head_dim]")
+    B, H, d = q.shape
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _expect(name, t, (B, H, d), q.dtype, dev)
+    _expect("log_alpha", log_alpha, (B, H), torch.float32, dev)
+    _expect("beta", beta, (B, H), torch.float32, dev)
+    S = state.shape[0]
+    _expect("state", state, (S, H, d, d), torch.float32, dev)
+    _expect("parent", parent, (B,), torch.int32, dev)
+    _expect("out", out, (B, H, d), q.dtype, dev)
+    _expect("state_out", state_out, (B, H, d, d), torch.float32, dev)
+    if parent is None and S < B:
+        raise ValueError(f"state: {S} states for {B} sequences")
+    _need_cuda(q, k, v, state)
+    with torch.cuda.device(dev):
+        out = torch.empty_like(q) if out is None else out
+        if state_out is None:
+            state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
+        _check("tg_gated_delta_step", library().tg_gated_delta_step(
+            _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(log_alpha), _ptr(beta), B, H, d,
+            float(eps), _ptr(state), S, _ptr(parent), _ptr(state_out), _ptr(out), _stream(dev)))
+    return out, state_out
+
+
+def beam_select_workspace(n_groups, beams, vocab, n_out, device=None):
+    """A workspace for beam_select of this shape (uint8 device tensor)."""
+    out = ctypes.c_size_t(0)
+    _check("tg_beam_select_workspace_bytes", library().tg_beam_select_workspace_bytes(
+        n_groups, beams, vocab, n_out, ctypes.byref(out)))
+    return torch.empty(int(out.value), dtype=torch.uint8, device=device or "cuda")
+
+
+def beam_select(logits, scores, n_out=None, workspace=None):
+    """The n_out (None: as many as beams) best continuations of each group of beams: logits
+    [groups * beams, vocab], scores [groups, beams] fp32 (a beam's score so far; -inf: no beam).
+
+    Returns (scores [groups, n_out] fp32 in order, parent [groups, n_out] int32 row of logits,
+    token [groups, n_out] int32); places without a candidate hold -inf, -1, -1.  parent is what
+    cache_update and gated_delta_step take.  workspace: beam_select_workspace(...) or None."""
+    if logits.dim() != 2 or scores.dim() != 2:
+        raise ValueError("logits must be [groups * beams, vocab], scores [groups, beams]")
+    G, beams = scores.shape
+    V = logits.shape[1]
+    dev = logits.device
+    _expect("logits", logits, (G * beams, V), logits.dtype, dev)
+    _expect("scores", scores, (G, beams), torch.float32, dev)
+    n_out = beams if n_out is None else int(n_out)
+    if workspace is not None:
+        _workspace(workspace, dev)
+    _need_cuda(logits, scores)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = beam_select_workspace(G, beams, V, n_out, dev)
+        best = torch.empty((G, n_out), dtype=torch.float32, device=dev)
+        parent, token = torch.empty((2, G, n_out), dtype=torch.int32, device=dev)
+        _check("tg_beam_select", library().tg_beam_select(
+            _ptr(logits), _dtype_code(logits), _ptr(scores), G, beams, V, n_out, _ptr(best),
+            _ptr(parent), _ptr(token), _ptr(workspace), workspace.numel(), _stream(dev)))
+    return best, parent, token

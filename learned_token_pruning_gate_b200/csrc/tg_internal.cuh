@@ -55,6 +55,7 @@ enum : uint32_t {
   kDevGatherIndex = 1u << 3,    // a kept index outside the prompt batch (row skipped)
   kDevTimeoutGather = 1u << 4,
   kDevTimeoutDelta = 1u << 5,   // a chunk load of the chunked delta-rule scan did not land
+  kDevPageIndex = 1u << 6,      // a page, length or parent outside its range in a decoding call (skipped)
 };
 
 // Host side: error reporting and the device status word.
@@ -127,6 +128,83 @@ tg_status launch_delta_chunked(const void* q, const void* k, const void* v, tg_d
                                const float* log_alpha, const float* beta, const PromptTable& pt,
                                int heads, int head_dim, float eps, void* out, float* state,
                                void* workspace, cudaStream_t st);
+// Decoding: attention over a paged cache, the cache's pages, a delta-rule step, beam selection.
+constexpr int kMaxSeqs = TG_MAX_SEQS;
+struct PagedAttnArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* table;
+  const int32_t* lens;
+  const float* logsig_pages;  // or null
+  const float* gain;
+  const float* temp;
+  void* out;
+  float* lse;  // or null
+  int32_t batch, hq, hkv, n_pages, max_pages;
+  int32_t page_shift;  // log2 of the page size
+  uint32_t* status;
+};
+tg_status launch_paged_attention(const PagedAttnArgs& a, tg_dtype dt, int head_dim, void* workspace,
+                                 cudaStream_t st);
+size_t paged_attention_workspace_bytes(tg_dtype dt, int batch, int hq, int hkv, int head_dim);
+struct CacheUpdateArgs {
+  const int32_t* table_in;
+  const int32_t* lens_in;
+  const int32_t* refs_in;
+  const int32_t* parent;  // or null
+  const int32_t* cu_new;  // or null
+  int32_t* table_out;
+  int32_t* lens_out;
+  int32_t* refs_out;
+  int32_t* start;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t batch_in, batch_out, n_pages, max_pages, page_shift;
+  uint32_t* status;
+};
+tg_status launch_cache_update(const CacheUpdateArgs& a, cudaStream_t st);
+struct CacheCompactArgs {
+  const int32_t* table_in;
+  const int32_t* lens;
+  const int32_t* refs_in;
+  int32_t* table_out;
+  int32_t* refs_out;
+  int32_t* page_map;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t* counts;
+  int32_t batch, n_pages, max_pages, page_shift;
+  uint32_t* status;
+};
+tg_status launch_cache_compact(const CacheCompactArgs& a, cudaStream_t st);
+tg_status launch_cache_copy(const tg_page_pool* pools, int n_pools, int n_pages, const int32_t* src,
+                            const int32_t* dst, int n_copies, const int32_t* count, uint32_t* status,
+                            cudaStream_t st);
+struct CacheAppendArgs {
+  const void* k;
+  const void* v;
+  const float* logsig;  // or null (zero)
+  const int32_t* cu_new;
+  const int32_t* start;
+  const int32_t* table;
+  void* k_pages;
+  void* v_pages;
+  float* logsig_pages;  // or null
+  int64_t rows;
+  int32_t batch, hkv, head_bytes, n_pages, max_pages, page_shift;
+  uint32_t* status;
+};
+tg_status launch_cache_append(const CacheAppendArgs& a, cudaStream_t st);
+tg_status launch_delta_step(const void* q, const void* k, const void* v, tg_dtype dt,
+                            const float* log_alpha, const float* beta, int batch, int heads,
+                            int head_dim, float eps, const float* state_in, int n_states,
+                            const int32_t* parent, float* state_out, void* out, uint32_t* status,
+                            cudaStream_t st);
+tg_status launch_beam_select(const void* logits, tg_dtype dt, const float* scores, int groups, int beams,
+                             int vocab, int n_out, float* scores_out, int32_t* parent_out,
+                             int32_t* token_out, void* workspace, cudaStream_t st);
+size_t beam_select_workspace_bytes(int groups, int beams, int vocab, int n_out);
 // Workspace the tensor-core attention uses to split long items on this device (0 = none).
 size_t attn_tc_workspace_bytes(const PromptTable& pt, int hq, int hkv, int dh);
 // The tg_attn_kernel the tensor-core attention launches for this batch.

@@ -281,3 +281,35 @@ def delta_inputs(M_list, H, d, seed, dtype="bf16", decay=0.1):
     la = torch.from_numpy(-rng.uniform(0.0, decay, (M, H)).astype(np.float32))
     beta = torch.from_numpy((1.0 / (1.0 + np.exp(-_normal(rng, (M, H))))).astype(np.float32))
     return cu, q, k, v, la, beta
+
+
+def paged_inputs(lens, Hq, Hkv, d, page, seed, dtype="bf16", max_pages=None, spare=3, fill=float("nan")):
+    """A paged cache with sequences of these lengths in scattered pages, and one query each:
+    dict of q, k_pages, v_pages, logsig_pages, table, lens, gain, temp.  What no token occupies
+    (spare pages, the rest of last pages) holds `fill` in k, v and the log-gates; table entries
+    behind a sequence's pages are -1."""
+    rng = np.random.Generator(np.random.Philox(seed))
+    t = _tdtype(dtype)
+    draw = lambda *shape: torch.from_numpy(_normal(rng, shape))  # noqa: E731
+    used = [-(-int(n) // page) for n in lens]
+    P = sum(used) + spare
+    width = max(used + [0]) + 1 if max_pages is None else max_pages
+    order = rng.permutation(P)
+    table = np.full((len(lens), width), -1, np.int32)
+    k = torch.full((P, Hkv, page, d), fill, dtype=t)
+    v = torch.full((P, Hkv, page, d), fill, dtype=t)
+    ls = torch.full((P, page), fill)
+    at = 0
+    for b, n in enumerate(lens):
+        table[b, :used[b]] = order[at:at + used[b]]
+        at += used[b]
+        for j in range(used[b]):
+            m = min(page, int(n) - j * page)
+            p = int(table[b, j])
+            k[p, :, :m] = draw(Hkv, m, d).to(t)
+            v[p, :, :m] = draw(Hkv, m, d).to(t)
+            ls[p, :m] = torch.nn.functional.logsigmoid(2.0 * draw(m))
+    return dict(q=draw(len(lens), Hq, d).to(t), k_pages=k, v_pages=v, logsig_pages=ls,
+                table=torch.from_numpy(table), lens=torch.tensor(list(lens), dtype=torch.int32),
+                gain=torch.from_numpy(rng.random(Hq, dtype=np.float32)),
+                temp=torch.from_numpy(0.8 + 0.4 * rng.random(Hq, dtype=np.float32)))
