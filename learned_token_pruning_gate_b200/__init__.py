@@ -18,7 +18,9 @@ together).
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -185,7 +187,20 @@ def _ptr(t):
 
 
 def _stream(device=None):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The raw handle of the current stream (of the tensors' device)."""
+    if device is not None and device.index is not None:
+        return torch._C._cuda_getCurrentRawStream(device.index)  # without a Stream object: 2 us less
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` current for a call; nothing to do when it is already."""
+    if torch.cuda.current_device() == device.index:
+        return _SAME_DEVICE
+    return torch.cuda.device(device)
 
 
 def _host_i32(a):
@@ -211,7 +226,8 @@ def _expect(name, t, shape, dtype, device):
     """A caller-passed tensor must match what the call reads or writes exactly:
     the kernels take raw pointers and trust the sizes derived from the other
     arguments, so a smaller buffer would be read or written past its end."""
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype is dtype and t.device == device
+                     and t.is_contiguous()):
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -767,7 +783,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=No
     if workspace is not None and not isinstance(workspace, str):
         _workspace(workspace, q.device)
     _need_cuda(q, k_pages, v_pages, table, lens)
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         one = torch.ones(Hq, device=q.device) if gain is None or temp is None else None
         gain = one if gain is None else gain
         temp = one if temp is None else temp
@@ -809,15 +825,15 @@ def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_o
                     ("copy_dst", copy_dst)):
         _expect(name, t, (Bo,), torch.int32, dev)
     _need_cuda(table, lens, refs)
-    with torch.cuda.device(dev):
+    with _on(dev):
         i32 = dict(dtype=torch.int32, device=dev)
         table_out = torch.full((Bo, mp), -1, **i32) if table_out is None else table_out
-        refs_out = torch.empty(P, **i32) if refs_out is None else refs_out
-        small = [lens_out, start, copy_src, copy_dst]
+        small = (refs_out, lens_out, start, copy_src, copy_dst)
         if any(t is None for t in small):
-            fresh = torch.empty((4, Bo), **i32)  # one allocation for those that are not given
-            small = [fresh[i] if t is None else t for i, t in enumerate(small)]
-        lens_out, start, copy_src, copy_dst = small
+            # one allocation for those that are not given
+            fresh = torch.empty(P + 4 * Bo, **i32).split((P, Bo, Bo, Bo, Bo))
+            small = [f if t is None else t for f, t in zip(fresh, small)]
+        refs_out, lens_out, start, copy_src, copy_dst = small
         _check("tg_cache_update", library().tg_cache_update(
             _ptr(table), _ptr(lens), B, _ptr(refs), P, page_size, mp, _ptr(parent), Bo,
             _ptr(cu_new), _ptr(table_out), _ptr(lens_out), _ptr(refs_out), _ptr(start),
@@ -839,12 +855,12 @@ def cache_compact(table, lens, refs, page_size, table_out=None, refs_out=None):
     _expect("table_out", table_out, (B, mp), torch.int32, dev)
     _expect("refs_out", refs_out, (P,), torch.int32, dev)
     _need_cuda(table, lens, refs)
-    with torch.cuda.device(dev):
+    with _on(dev):
         i32 = dict(dtype=torch.int32, device=dev)
         table_out = torch.full((B, mp), -1, **i32) if table_out is None else table_out
-        refs_out = torch.empty(P, **i32) if refs_out is None else refs_out
-        page_map, src, dst = torch.empty((3, P), **i32)
-        counts = torch.empty(2, **i32)
+        fresh = torch.empty(4 * P + 2, **i32).split((P, P, P, P, 2))
+        page_map, src, dst, counts = fresh[1:]
+        refs_out = fresh[0] if refs_out is None else refs_out
         _check("tg_cache_compact", library().tg_cache_compact(
             _ptr(table), _ptr(lens), B, _ptr(refs), P, page_size, mp, _ptr(table_out),
             _ptr(refs_out), _ptr(page_map), _ptr(src), _ptr(dst), _ptr(counts), _stream(dev)))
@@ -871,10 +887,10 @@ def cache_copy_pages(pools, copy_src, copy_dst, count=None):
             raise ValueError(f"pools[{i}]: shape {tuple(t.shape)}, expected [layers, {P}, ...]")
         _expect(f"pools[{i}]", t, t.shape, t.dtype, dev)
         arr[i].base = t.data_ptr()
-        arr[i].page_bytes = int(np.prod(t.shape[2:], dtype=np.int64)) * t.element_size()
+        arr[i].page_bytes = math.prod(t.shape[2:]) * t.element_size()
         arr[i].layers = t.shape[0]
     _need_cuda(copy_src, *pools)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check("tg_cache_copy_pages", library().tg_cache_copy_pages(
             arr, len(pools), P, _ptr(copy_src), _ptr(copy_dst), n, _ptr(count), _stream(dev)))
 
@@ -896,7 +912,7 @@ def cache_append(k, v, cu_new, start, table, k_pages, v_pages, logsig=None, logs
     _expect("cu_new", cu_new, (B + 1,), torch.int32, dev)
     _expect("start", start, (B,), torch.int32, dev)
     _need_cuda(k, v, cu_new, start, table, k_pages)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check("tg_cache_append", library().tg_cache_append(
             _ptr(k), _ptr(v), _ptr(logsig), _dtype_code(k), rows, B, _ptr(cu_new), _ptr(start),
             Hkv, d, P, page, _ptr(table), mp, _ptr(k_pages), _ptr(v_pages), _ptr(logsig_pages),
@@ -928,7 +944,7 @@ def gated_delta_step(q, k, v, log_alpha, beta, state, parent=None, eps=1e-6, out
     if parent is None and S < B:
         raise ValueError(f"state: {S} states for {B} sequences")
     _need_cuda(q, k, v, state)
-    with torch.cuda.device(dev):
+    with _on(dev):
         out = torch.empty_like(q) if out is None else out
         if state_out is None:
             state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
@@ -964,11 +980,11 @@ def beam_select(logits, scores, n_out=None, workspace=None):
     if workspace is not None:
         _workspace(workspace, dev)
     _need_cuda(logits, scores)
-    with torch.cuda.device(dev):
+    with _on(dev):
         if workspace is None:
             workspace = beam_select_workspace(G, beams, V, n_out, dev)
         best = torch.empty((G, n_out), dtype=torch.float32, device=dev)
-        parent, token = torch.empty((2, G, n_out), dtype=torch.int32, device=dev)
+        parent, token = torch.empty((2, G, n_out), dtype=torch.int32, device=dev).unbind()
         _check("tg_beam_select", library().tg_beam_select(
             _ptr(logits), _dtype_code(logits), _ptr(scores), G, beams, V, n_out, _ptr(best),
             _ptr(parent), _ptr(token), _ptr(workspace), workspace.numel(), _stream(dev)))

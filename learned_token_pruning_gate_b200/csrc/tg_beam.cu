@@ -2,20 +2,21 @@
 // the beam's score added, and the n best of beams x vocabulary in order.
 //
 // Within a beam the order of the candidates is the order of the logits, so the
-// vocabulary is read once: beam_chunk_kernel takes 8192 logits of one row into
+// vocabulary is read once: beam_chunk_kernel takes 32 KB of one row into
 // registers and leaves the chunk's maximum, its sum of exponentials and its n
 // best logits, sorted.  beam_merge_kernel, one CTA per group, joins the sums
 // into the rows' log-sums in 64 bits and picks the n best of the lists.
 //
-// Both pick by a threshold: among the largest keys of disjoint sets (a thread's
-// logits; a sorted list) the n-th largest is a lower bound on the n-th best
-// overall, so only keys not below it are collected (rarely more than 2 n), and
-// a collected key's place is the number of larger ones.  Keys are distinct,
-// since the index is part of them, so ties go to the lower index and the order
-// of collection does not matter.
+// Both pick by a threshold, a lower bound on the n-th best: among the largest of
+// disjoint sets (a thread's logits; a sorted list) the n-th largest is one.  Only
+// what is not below it is collected (rarely more than 2 n), and a collected key's
+// place is the number of larger ones.  Keys are distinct, since the index is part
+// of them, so ties go to the lower index and the order of collection does not
+// matter.  A chunk finds its threshold by bisection over the threads' maxima, one
+// barrier with a count per step; it stops as soon as the count is close to n.
 //
 // The scores are compared in 64 bits: beams meet at sums that differ in the last
-// places of 32, and a chunk's sum in 32 bits (32 terms per thread, then a tree)
+// places of 32, and a chunk's sum in 32 bits (at most 64 terms per thread, then a tree)
 // is off by less than 1e-7 of itself.
 #include <cmath>
 
@@ -25,40 +26,108 @@ namespace tg {
 namespace {
 
 constexpr int kChunkThreads = 256;
-constexpr int kPerThread = 32;
-constexpr int kChunk = kChunkThreads * kPerThread;  // logits per CTA
 constexpr int kMaxOut = 2 * TG_MAX_BEAMS;
-// Collected keys: fewer than n threads whose largest is above the threshold, with 32 each, and
-// the threshold itself; fewer than n threads with any key, when there is no threshold.
-constexpr int kChunkKeys = kMaxOut * kPerThread;
-constexpr int kMergeThreads = 1024;
-// Likewise: at most n lists of n keys each.
-constexpr int kMergeKeys = kMaxOut * kMaxOut;
+// Logits per thread and per CTA: 128 bytes a thread.
+template <typename T>
+constexpr int kPerThread = 128 / static_cast<int>(sizeof(T));
+template <typename T>
+constexpr int kChunk = kChunkThreads * kPerThread<T>;
+constexpr int kChunkKeys = 2048;  // room for a chunk's collected keys
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kInvLog2e = 1.0 / kLog2e;
+constexpr int kMergeThreads = 512;
 
-// What a chunk leaves: per (row, chunk) its maximum and sum, and n keys.
+// What a chunk leaves: per (row, chunk) n keys, and {c, sum 2^(x log2e - c)}, with c the
+// rounded maximum times log2e as fp32 has it (-inf: no finite logit).
 struct BeamWork {
   float2* sums;
   uint64_t* keys;
 };
 
-__host__ __device__ inline int chunks_of(int vocab, int vec) { return (vocab + vec - 1 + kChunk - 1) / kChunk; }
+// A thread's logits as they come from memory: 16-byte pieces, unpacked where they are used, so
+// that bf16 ones take half the registers.
+template <typename T>
+struct Logits {
+  static constexpr int kN = kPerThread<T>;
+  uint32_t w[32];
+  static constexpr bool kHalf = sizeof(T) == 2;
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (kHalf) return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    else return __uint_as_float(w[e]);
+  }
+  __device__ __forceinline__ void set(int e, float x) {  // x is a number of type T
+    const uint32_t b = __float_as_uint(x);
+    if constexpr (kHalf) w[e >> 1] = e & 1 ? (w[e >> 1] & 0xffffu) | (b & 0xffff0000u) : (w[e >> 1] & 0xffff0000u) | (b >> 16);
+    else w[e] = b;
+  }
+  __device__ __forceinline__ float largest() const {  // (NaN is passed over)
+    if constexpr (kHalf) {
+      __nv_bfloat162 m, x;
+      memcpy(&m, &w[0], 4);
+#pragma unroll
+      for (int e = 1; e < 32; ++e) {
+        memcpy(&x, &w[e], 4);
+        m = __hmax2(m, x);
+      }
+      return fmaxf(__low2float(m), __high2float(m));
+    } else {
+      float m = get(0);
+#pragma unroll
+      for (int e = 1; e < 32; ++e) m = fmaxf(m, get(e));
+      return m;
+    }
+  }
+  // Which logits are not below `bound`: bits[0] and bits[1] name the elements first(b) and up.
+  __device__ __forceinline__ void not_below(float bound, uint32_t (&bits)[2]) const {
+    bits[0] = bits[1] = 0;
+    if constexpr (kHalf) {
+      const __nv_bfloat162 b = __bfloat162bfloat162(__float2bfloat16_ru(bound));
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        __nv_bfloat162 x;
+        memcpy(&x, &w[e], 4);
+        bits[e >> 4] |= __hge2_mask(x, b) & (0x00010001u << (e & 15));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (get(e) >= bound) bits[0] |= 1u << e;
+    }
+  }
+  // The element that bit b of bits[half] stands for.
+  static __device__ __forceinline__ int element(int half, int b) {
+    return kHalf ? half * 32 + (b & 15) * 2 + (b >> 4) : b;
+  }
+};
+
+template <typename T>
+__host__ __device__ inline int chunks_of(int vocab) {
+  return (vocab + 16 / static_cast<int>(sizeof(T)) - 1 + kChunk<T> - 1) / kChunk<T>;
+}
 
 // Larger logit first, then the lower token; 0 for what is no candidate.
 __device__ __forceinline__ uint64_t logit_key(float x, int token) {
   if (!(x > -INFINITY)) return 0;  // -inf, NaN
   return (static_cast<uint64_t>(order_key(x)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(token));
 }
+// The number whose order_key is k (k > 0).
+__device__ __forceinline__ float from_order_key(uint32_t k) {
+  return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
+}
+constexpr uint32_t kLowestKey = 0x00800000u;  // order_key of the lowest finite number
 
 template <typename T>
-__global__ void __launch_bounds__(kChunkThreads)
+__global__ void __launch_bounds__(kChunkThreads, 4)
     beam_chunk_kernel(const T* __restrict__ logits, int vocab, int n_out, int chunks, BeamWork ws) {
+  using L = Logits<T>;
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-  constexpr int kVecs = kPerThread / kVec;
-  __shared__ __align__(16) uint64_t heads[kChunkThreads];
+  constexpr int kWarps = kChunkThreads / 32;
+  static_assert(kChunkKeys >= (kMaxOut - 1) * 32, "most logits of a chunk in which fewer than n threads have any");
   __shared__ __align__(16) uint64_t found[kChunkKeys];
-  __shared__ uint64_t floor_key;
   __shared__ int n_found;
-  __shared__ float red[kChunkThreads / 32];
+  __shared__ uint32_t red_max[kWarps], red_min[kWarps];
+  __shared__ float red_sum[kWarps];
+  __shared__ uint64_t red_key[kWarps];
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -67,99 +136,124 @@ __global__ void __launch_bounds__(kChunkThreads)
   // A row may start anywhere: its 16-byte pieces begin at the boundary at or before it, `lead` tokens early.
   const T* r = logits + row * vocab;
   const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
-  float x[kPerThread];
-  const int t0 = chunk * kChunk - lead;  // token of the chunk's first element
+  const int t0 = chunk * kChunk<T> - lead + tid * kVec;  // token of the thread's first element
+  auto token = [&](int e) { return t0 + (e / kVec) * (kChunkThreads * kVec) + e % kVec; };
+  L x;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int t = t0 + (i * kChunkThreads + tid) * kVec;
+  for (int i = 0; i < 8; ++i) {
+    const int t = t0 + i * kChunkThreads * kVec;
     if (t >= 0 && t + kVec <= vocab) {
-      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(r + t));
-      if constexpr (sizeof(T) == 4) {
-        x[i * kVec] = __uint_as_float(u.x);
-        x[i * kVec + 1] = __uint_as_float(u.y);
-        x[i * kVec + 2] = __uint_as_float(u.z);
-        x[i * kVec + 3] = __uint_as_float(u.w);
-      } else {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[i * kVec + 2 * e] = __uint_as_float(w[e] << 16);
-          x[i * kVec + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
-      }
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(r + t));
+      x.w[4 * i] = u.x;
+      x.w[4 * i + 1] = u.y;
+      x.w[4 * i + 2] = u.z;
+      x.w[4 * i + 3] = u.w;
     } else {
 #pragma unroll
       for (int e = 0; e < kVec; ++e)
-        x[i * kVec + e] = t + e >= 0 && t + e < vocab ? static_cast<float>(r[t + e]) : -INFINITY;
+        x.set(i * kVec + e, t + e >= 0 && t + e < vocab ? static_cast<float>(r[t + e]) : -INFINITY);
     }
   }
-  auto token = [&](int e) { return t0 + ((e / kVec) * kChunkThreads + tid) * kVec + e % kVec; };
 
-  // the chunk's maximum; the thread's largest key
-  float m = x[0];
-  int at = 0;
-#pragma unroll
-  for (int e = 1; e < kPerThread; ++e)
-    if (x[e] > m || m != m) {
-      m = x[e];
-      at = e;
-    }
-  // (the scan above goes up in e, and the token goes up with e, so equal logits keep the lower one)
-  uint64_t best = 0;
-#pragma unroll
-  for (int e = 0; e < kPerThread; ++e)
-    if (e == at) best = logit_key(m, token(e));
-  heads[tid] = best;
-  float top = m == m ? m : -INFINITY;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) red[warp] = top;
-  if (tid == 0) {
-    floor_key = 1;
-    n_found = 0;
+  // the thread's largest logit; the largest and smallest of these in the chunk
+  const uint32_t key = order_key(x.largest());
+  const uint32_t warp_max = __reduce_max_sync(0xffffffffu, key), warp_min = __reduce_min_sync(0xffffffffu, key);
+  if (lane == 0) {
+    red_max[warp] = warp_max;
+    red_min[warp] = warp_min;
   }
+  if (tid == 0) n_found = 0;
   __syncthreads();
+  const uint32_t top = __reduce_max_sync(0xffffffffu, red_max[lane % kWarps]);
+  const uint32_t low = __reduce_min_sync(0xffffffffu, red_min[lane % kWarps]);
+  // Sum of exponentials, 2^(x log2e - c) with one rounding each: c is a number the merge knows
+  // exactly, so rounding the maximum does not shift the sum.  NaN and +inf make it NaN; a chunk
+  // without a logit above -inf leaves 0.
+  const float largest = top >= kLowestKey ? from_order_key(top) : -INFINITY;
+  const float c = largest * kLog2e;
+  const float minus_c = largest == -INFINITY ? 0.0f : -c;
+  float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int w = 0; w < kChunkThreads / 32; ++w) top = fmaxf(top, red[w]);
-  // sum of exponentials; NaN and +inf make it NaN, an empty chunk leaves 0
-  float s = 0.0f;
-  const float shift = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-  for (int e = 0; e < kPerThread; ++e) s += exp2_approx((x[e] - shift) * 1.4426950408889634f);
+  for (int e = 0; e < L::kN; e += 2) {
+    const float2 y = __ffma2_rn(make_float2(x.get(e), x.get(e + 1)), make_float2(kLog2e, kLog2e),
+                                make_float2(minus_c, minus_c));
+    s2 = __fadd2_rn(s2, make_float2(exp2_approx(y.x), exp2_approx(y.y)));
+  }
+  float s = s2.x + s2.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  // the n-th largest of the threads' keys is the floor
-  if (best) {
-    int above = 0;
-#pragma unroll 8
-    for (int j = 0; j < kChunkThreads; ++j) above += heads[j] > best;
-    if (above == n_out - 1) floor_key = best;
-  }
-  __syncthreads();
-  if (lane == 0) red[warp] = s;
-  const uint64_t fl = floor_key;
-  if (best >= fl) {
-#pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      const uint64_t key = logit_key(x[e], token(e));
-      if (key >= fl) found[atomicAdd(&n_found, 1)] = key;
+  if (lane == 0) red_sum[warp] = s;
+
+  // The threshold lo: at least n threads hold a logit not below it (or it is the lowest finite
+  // number).  Bisection between the chunk's smallest and largest thread maximum.
+  uint32_t lo = max(low, kLowestKey), hi = top + 1;
+  if (__syncthreads_count(key >= lo) >= n_out) {
+    const int enough = n_out + (n_out >> 1) + 4;
+    while (hi - lo > 1) {
+      const uint32_t mid = lo + ((hi - lo) >> 1);
+      const int above = __syncthreads_count(key >= mid);
+      if (above >= n_out) {
+        lo = mid;
+        if (above <= enough) break;
+      } else {
+        hi = mid;
+      }
     }
+  } else {
+    lo = kLowestKey;
+  }
+  if (key >= lo) {
+    uint32_t bits[2];
+    x.not_below(from_order_key(lo), bits);
+#pragma unroll
+    for (int half = 0; half < L::kN / 32; ++half)
+      for (uint32_t b = bits[half]; b; b &= b - 1) {
+        const int at = atomicAdd(&n_found, 1);
+        const int t = token(L::element(half, __ffs(b) - 1));
+        if (at < kChunkKeys) found[at] = logit_key(static_cast<float>(r[t]), t);
+      }
   }
   __syncthreads();
   const int n = n_found;
   uint64_t* out = ws.keys + (row * chunks + chunk) * n_out;
-  for (int i = tid; i < n; i += kChunkThreads) {
-    const uint64_t key = found[i];
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += found[j] > key;
-    if (above < n_out) out[above] = key;
+  if (n <= kChunkKeys) {
+    for (int i = tid; i < n; i += kChunkThreads) {
+      const uint64_t k = found[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j) above += found[j] > k;
+      if (above < n_out) out[above] = k;
+    }
+    for (int i = n + tid; i < n_out; i += kChunkThreads) out[i] = 0;
+  } else {
+    // More logits than there is room for share the threshold (a flat row): one best after another.
+    uint64_t last = ~0ull;
+    for (int i = 0; i < n_out; ++i) {
+      uint64_t k = 0;
+#pragma unroll 1
+      for (int e = 0; e < L::kN; ++e) {
+        const int t = token(e);
+        if (t < 0 || t >= vocab) continue;
+        const uint64_t one = logit_key(static_cast<float>(r[t]), t);
+        if (one < last && one > k) k = one;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, k, o);
+        k = other > k ? other : k;
+      }
+      if (lane == 0) red_key[warp] = k;
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w) k = red_key[w] > k ? red_key[w] : k;
+      if (tid == 0) out[i] = k;
+      last = k;
+      __syncthreads();
+    }
   }
-  for (int i = n + tid; i < n_out; i += kChunkThreads) out[i] = 0;
   if (tid == 0) {
     float total = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kChunkThreads / 32; ++w) total += red[w];
-    ws.sums[row * chunks + chunk] = make_float2(top, total);
+    for (int w = 0; w < kWarps; ++w) total += red_sum[w];
+    ws.sums[row * chunks + chunk] = make_float2(c, total);
   }
 }
 
@@ -179,10 +273,7 @@ __device__ __forceinline__ uint64_t order_key64(double x) {
 __device__ __forceinline__ double from_order_key64(uint64_t k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k));
 }
-__device__ __forceinline__ float logit_of(uint64_t key) {
-  const uint32_t k = static_cast<uint32_t>(key >> 32);
-  return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
-}
+__device__ __forceinline__ float logit_of(uint64_t key) { return from_order_key(static_cast<uint32_t>(key >> 32)); }
 
 __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const float* __restrict__ scores, int beams, int vocab, int n_out, int chunks,
@@ -190,25 +281,29 @@ __global__ void __launch_bounds__(kMergeThreads)
                       int32_t* __restrict__ token_out) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int lists = beams * chunks;
-  uint64_t* const head_score = reinterpret_cast<uint64_t*>(smem);          // [lists]
-  uint64_t* const found_score = head_score + lists;                        // [kMergeKeys]
-  uint32_t* const head_place = reinterpret_cast<uint32_t*>(found_score + kMergeKeys);  // [lists]
-  uint32_t* const found_place = head_place + lists;                        // [kMergeKeys]
+  const int room = n_out * (n_out + 1) / 2;
+  uint64_t* const head_score = reinterpret_cast<uint64_t*>(smem);                // [lists]
+  uint64_t* const found_score = head_score + lists;                              // [room]
+  uint32_t* const head_place = reinterpret_cast<uint32_t*>(found_score + room);  // [lists]
+  uint32_t* const found_place = head_place + lists;                              // [room]
   __shared__ double log_sum[TG_MAX_BEAMS];
-  __shared__ Cand fl;
+  __shared__ int ranked[kMaxOut];  // the lists by their heads
+  __shared__ Cand limit;           // the n-th head
   __shared__ int n_found;
   grid_dep_wait();
   grid_dep_launch();
-  const int tid = threadIdx.x, lane = tid & 31;
+  constexpr int kWarps = kMergeThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * beams;
   if (tid == 0) {
-    fl.score = 1;
-    fl.place = 0xFFFFFFFFu;
+    limit.score = 1;
+    limit.place = 0xFFFFFFFFu;
     n_found = 0;
   }
+  if (tid < kMaxOut) ranked[tid] = -1;
   // a warp per beam: log of the row's sum of exponentials
-  if ((tid >> 5) < beams) {
-    const float2* part = ws.sums + (row0 + (tid >> 5)) * chunks;
+  for (int beam = warp; beam < beams; beam += kWarps) {
+    const float2* part = ws.sums + (row0 + beam) * chunks;
     float top = -INFINITY;
     for (int c = lane; c < chunks; c += 32) top = fmaxf(top, part[c].x);
 #pragma unroll
@@ -216,11 +311,12 @@ __global__ void __launch_bounds__(kMergeThreads)
     double s = 0.0;
     for (int c = lane; c < chunks; c += 32) {
       const float2 p = part[c];
-      if (p.y != 0.0f) s += static_cast<double>(p.y) * exp(static_cast<double>(p.x) - top);  // NaN stays NaN
+      // (the chunks' c are multiples of log2e as fp32 has it)
+      if (p.y != 0.0f) s += static_cast<double>(p.y) * exp((static_cast<double>(p.x) - top) * kInvLog2e);  // NaN stays NaN
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) log_sum[tid >> 5] = static_cast<double>(top) + log(s);
+    if (lane == 0) log_sum[beam] = static_cast<double>(top) * kInvLog2e + log(s);
   }
   __syncthreads();
   auto cand = [&](int list, int i) {
@@ -240,33 +336,41 @@ __global__ void __launch_bounds__(kMergeThreads)
     head_place[l] = c.place;
   }
   __syncthreads();
-  for (int l = tid; l < lists; l += kMergeThreads) {
+  // a warp per head: how many heads come before it
+  for (int l = warp; l < lists; l += kWarps) {
     const Cand c = {head_score[l], head_place[l]};
     if (!c.score) continue;
     int above = 0;
-    for (int j = 0; j < lists; ++j) above += before(Cand{head_score[j], head_place[j]}, c);
-    if (above == n_out - 1) fl = c;
+    for (int j = lane; j < lists; j += 32) above += before(Cand{head_score[j], head_place[j]}, c);
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane == 0 && above < n_out) {
+      ranked[above] = l;
+      if (above == n_out - 1) limit = c;
+    }
   }
   __syncthreads();
-  const Cand limit = fl;
-  for (int i = tid; i < lists * n_out; i += kMergeThreads) {
-    const int l = i / n_out;
-    const Cand h = {head_score[l], head_place[l]};
-    if (!h.score || before(limit, h)) continue;  // nothing of this list reaches the floor
-    const Cand c = cand(l, i - l * n_out);
-    if (!c.score || before(limit, c)) continue;
-    const int at = atomicAdd(&n_found, 1);
-    found_score[at] = c.score;
-    found_place[at] = c.place;
+  // The list whose head is r-th can add n - r candidates: r heads and its own earlier ones come
+  // before the others.  Of these the ones not behind the n-th head count.
+  for (int r = warp; r < n_out; r += kWarps) {
+    const int l = ranked[r];
+    if (l < 0) break;
+    for (int i = lane; i < n_out - r; i += 32) {
+      const Cand c = cand(l, i);
+      if (!c.score || before(limit, c)) continue;
+      const int at = atomicAdd(&n_found, 1);
+      found_score[at] = c.score;
+      found_place[at] = c.place;
+    }
   }
   __syncthreads();
   const int n = n_found;
   const int64_t out = static_cast<int64_t>(blockIdx.x) * n_out;
-  for (int i = tid; i < n; i += kMergeThreads) {
+  for (int i = warp; i < n; i += kWarps) {
     const Cand c = {found_score[i], found_place[i]};
     int above = 0;
-    for (int j = 0; j < n; ++j) above += before(Cand{found_score[j], found_place[j]}, c);
-    if (above >= n_out) continue;
+    for (int j = lane; j < n; j += 32) above += before(Cand{found_score[j], found_place[j]}, c);
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (lane != 0 || above >= n_out) continue;
     const uint32_t beam = c.place / static_cast<uint32_t>(vocab);
     scores_out[out + above] = static_cast<float>(from_order_key64(c.score));
     parent_out[out + above] = static_cast<int32_t>(row0 + beam);
@@ -279,20 +383,17 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
 }
 
-// The chunks of a row at the wider of the two element counts per 16 bytes, for either dtype.
-int max_chunks(int vocab) { return chunks_of(vocab, 8); }
-
 }  // namespace
 
 size_t beam_select_workspace_bytes(int groups, int beams, int vocab, int n_out) {
-  const size_t lists = static_cast<size_t>(groups) * beams * max_chunks(vocab);
+  const size_t lists = static_cast<size_t>(groups) * beams * chunks_of<float>(vocab);  // (bf16 takes fewer)
   return (lists * sizeof(float2) + 15) / 16 * 16 + lists * n_out * sizeof(uint64_t);
 }
 
 tg_status launch_beam_select(const void* logits, tg_dtype dt, const float* scores, int groups, int beams,
                              int vocab, int n_out, float* scores_out, int32_t* parent_out,
                              int32_t* token_out, void* workspace, cudaStream_t st) {
-  const int chunks = max_chunks(vocab);
+  const int chunks = dt == TG_BF16 ? chunks_of<__nv_bfloat16>(vocab) : chunks_of<float>(vocab);
   const size_t lists = static_cast<size_t>(groups) * beams * chunks;
   BeamWork ws;
   ws.sums = static_cast<float2*>(workspace);
@@ -305,9 +406,12 @@ tg_status launch_beam_select(const void* logits, tg_dtype dt, const float* score
           : launch_pdl(beam_chunk_kernel<float>, grid, dim3(kChunkThreads), 0, st,
                        static_cast<const float*>(logits), vocab, n_out, chunks, ws);
   if (e != cudaSuccess) return cuda_check(e, "beam chunk launch");
-  const size_t smem = (static_cast<size_t>(beams) * chunks + kMergeKeys) * (sizeof(uint64_t) + sizeof(uint32_t));
-  e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return cuda_check(e, "beam merge shared memory");
+  const size_t per_group = static_cast<size_t>(beams) * chunks;
+  const size_t smem = (per_group + n_out * (n_out + 1) / 2) * (sizeof(uint64_t) + sizeof(uint32_t));
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return cuda_check(e, "beam merge shared memory");
+  }
   return cuda_check(launch_pdl(beam_merge_kernel, dim3(static_cast<unsigned>(groups)), dim3(kMergeThreads), smem,
                                st, scores, beams, vocab, n_out, chunks, ws, scores_out, parent_out, token_out),
                     "beam merge launch");
