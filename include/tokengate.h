@@ -563,10 +563,9 @@ TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int3
  *   workspace, workspace_bytes
  *         device scratch of tg_paged_attention_workspace_bytes, or NULL.  With it
  *         the keys of a sequence are split over several SMs and joined in a fixed
- *         order; without it one SM reads them all.  16-byte aligned; zeroed once
- *         by the caller after allocating it, every call leaves its counters
- *         zero again.  TG_ERR_WORKSPACE when smaller.  Calls that share a
- *         workspace must not overlap on the GPU.
+ *         order; without it one SM reads them all.  16-byte aligned, any
+ *         contents.  TG_ERR_WORKSPACE when smaller.  Calls that share a workspace
+ *         must not overlap on the GPU.
  *   head_dim 64 or 128, 16-byte aligned q, k_pages, v_pages and out.
  */
 TG_API tg_status tg_paged_attention(const void* q, const void* k_pages, const void* v_pages,

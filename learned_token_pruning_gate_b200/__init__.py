@@ -744,15 +744,15 @@ def _table(table, lens, device):
 
 def paged_attention_workspace(batch, n_q_heads, n_kv_heads, head_dim, dtype=torch.bfloat16,
                               device=None):
-    """A zeroed workspace for paged_attention of this shape (uint8 device tensor): with it a
-    sequence's keys are split over several SMs.  Calls on it must not overlap on the GPU."""
+    """A workspace for paged_attention of this shape (uint8 device tensor): with it a sequence's
+    keys are split over several SMs.  Calls on it must not overlap on the GPU."""
     device = torch.device(device or "cuda")
     out = ctypes.c_size_t(0)
     with torch.cuda.device(device):
         _check("tg_paged_attention_workspace_bytes", library().tg_paged_attention_workspace_bytes(
             TG_BF16 if dtype in ("bf16", torch.bfloat16) else TG_FP32, batch, n_q_heads,
             n_kv_heads, head_dim, ctypes.byref(out)))
-        return torch.zeros(int(out.value), dtype=torch.uint8, device=device)
+        return torch.empty(int(out.value), dtype=torch.uint8, device=device)
 
 
 def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=None, temp=None,
@@ -761,7 +761,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=No
 
     q [B, Hq, d]; k_pages, v_pages [P, Hkv, page, d]; table [B, max_pages] and lens [B] int32 on
     the device; logsig_pages [P, page] or None (no bias); gain (None: 1), temp (None: 1) [Hq].
-    workspace: "auto" (allocate and zero one), None (no split), or paged_attention_workspace(...),
+    workspace: "auto" (allocate one), None (no split), or paged_attention_workspace(...),
     which a decoding loop keeps.  Returns (out [B, Hq, d], lse [Hq, B] or None)."""
     if q.dim() != 3:
         raise ValueError("q must be [batch, heads, head_dim]")

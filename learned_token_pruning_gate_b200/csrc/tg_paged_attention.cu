@@ -6,16 +6,20 @@
 // matters is that all SMs read all the time, whatever the lengths.
 //
 // Work: a unit is (sequence, kv head, block of its query heads), cut into tiles of
-// 64 keys.  The tiles of all units form one list, and every CTA takes an equal run
-// of it, computed from the lengths on the device.  A CTA that holds a unit whole
-// writes its output; a unit that several CTAs share is joined from their partial
-// sums (running maximum, sum, weighted v) by the last of them to arrive, in the
-// order of the list, so the result does not depend on the schedule.
+// 64 keys (128 of bf16 rows of 64 columns).  The tiles of all units form one list,
+// and every CTA takes an equal run of it, computed from the lengths on the device.
+// A CTA that holds a unit whole writes its output; the partial sums (reference
+// maximum, sum, weighted v) of a unit that several CTAs share are joined by a
+// second kernel in the order of the list, so the result does not depend on the
+// schedule.  (Joined by the last CTA to arrive instead, a call of one sequence took
+// 8.6 us for 7.1, and 64 parts of 8 heads 18 us longer: the fence, the counter and
+// one SM reading all parts are slower than a dependent launch.)
 //
-// Within a tile a warp takes 16 keys, which lie in one page.  There is no shared
-// memory on the way: rows go from HBM to registers in 16-byte pieces, the next
-// 16 keys' K is requested as soon as this one's products are issued, and V
-// likewise, so a warp has 4 to 8 KB in flight at all times.
+// Within a tile a warp takes 16 keys of one page at a time (two such groups where
+// rows are short, so that as much is in flight).  There is no shared memory on the
+// way: rows go from HBM to registers in 16-byte pieces, the next keys' K is
+// requested as soon as this one's products are issued, and V likewise, across unit
+// boundaries too, so a warp has 4 to 8 KB in flight at all times.
 //
 // bf16: the legacy m16n8k16 tensor instruction with keys as its 16 rows and query
 // heads as its 8 columns: S^T = K Q^T, O^T = V^T P.  Its fragments can be had
@@ -41,7 +45,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 16 * kWarps;  // keys of a tile, 16 per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // how far a logit may exceed the reference maximum
 
@@ -60,7 +63,8 @@ struct Plan {
   int32_t group;       // query heads per kv head
   int32_t blocks;      // blocks of query heads per kv head
   int32_t units;       // units per sequence: hkv * blocks
-  int32_t* counters;   // [batch * units], or null: no unit is shared
+  int2* shares;        // [batch * units] the first and last CTA of a shared unit, {0, -1} otherwise; or null:
+                       // every unit is whole
   float* partial;      // [2 * grid][heads][d + 2]
 };
 
@@ -93,11 +97,11 @@ __device__ __forceinline__ float weight(float x, float m) {
   return exp2_approx((x - (m == -INFINITY ? 0.0f : m)) * kLog2e);
 }
 
-// A warp's 16 keys of one page: where they are, how many count, their log-gates.
+// A warp's 16 keys of one page: where they are, and how many of them count.
 struct Keys {
   int64_t row;   // first row: (page * hkv + kv head) * page size + offset
-  int32_t n;     // keys below the length; 0 when the page is not to be read
   int64_t gate;  // first log-gate
+  int32_t n;     // keys below the length; 0 when the page is not to be read
 };
 
 __device__ __forceinline__ Keys locate(const Plan& p, int b, int hk, int len, int key, bool* bad) {
@@ -115,72 +119,43 @@ __device__ __forceinline__ Keys locate(const Plan& p, int b, int hk, int len, in
   return k;
 }
 
-// ---- bf16: a warp's share of a segment -----------------------------------------------------------
+// ---- bf16: 16 R keys of a warp ---------------------------------------------------------------------
 // Columns of the instruction are query heads.  The weights enter the second product as the sum
 // of two bf16 numbers (the weight rounded, and what that cut off), so that the output is off by
 // little more than its own rounding; the extra products cost no memory time.
 template <int D, int NT>
 struct CoreBf16 {
   static constexpr int kHeads = 8 * NT;
+  static constexpr int R = 128 / D;   // groups of 16 keys
+  static constexpr int kKeys = 16 * R;
+  static constexpr int kSteps = 1;
   static constexpr int kKv = D / 32;  // 16-byte pieces per lane and row half, for K and for Q
   static constexpr int kVv = D / 64;  // 16-byte pieces per lane and key, for V
-  static constexpr int kMinCtas = ctas_per_sm(true, kHeads, D);
 
-  static __device__ __forceinline__ void run(const Plan& p, int b, int hk, int h0, int nh, int key0, int key_end,
-                                             int len, float* part_m, float* part_l, float* part_o, bool* bad) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(p.a.k_pages);
-    const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(p.a.v_pages);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 q[NT][kKv], k[R][2][kKv], v[R][4][kVv];
+  float gate[R][2], scale[NT][2], gain[NT][2], m[NT][2], l[NT][2], o[NT][D / 16][4];
+  float s[R][NT][4];
 
-    Keys at = locate(p, b, hk, min(len, key_end), key0 + warp * 16, bad);
-    uint4 k[2][kKv], v[4][kVv];
-    float gate[2];
-    auto load_k = [&](const Keys& s) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const bool in = g + 8 * r < s.n;
-        const __nv_bfloat16* src = kp + (s.row + g + 8 * r) * D + t * 8;
-#pragma unroll
-        for (int c = 0; c < kKv; ++c) k[r][c] = in ? load_row16(src + c * 32) : zero;
-        gate[r] = !in ? -INFINITY : p.a.logsig_pages ? p.a.logsig_pages[s.gate + g + 8 * r] : 0.0f;
-      }
-    };
-    auto load_v = [&](const Keys& s) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 2 * t + (i & 1) + 8 * (i >> 1);
-        const __nv_bfloat16* src = vp + (s.row + key) * D + g * 8;
-#pragma unroll
-        for (int c = 0; c < kVv; ++c) v[i][c] = key < s.n ? load_row16(src + c * 64) : zero;
-      }
-    };
-    load_k(at);
-    load_v(at);
+  static __device__ __forceinline__ int g() { return (threadIdx.x & 31) >> 2; }
+  static __device__ __forceinline__ int t() { return threadIdx.x & 3; }
 
-    // the query rows as B fragments: column g of tile n is head h0 + 8 n + g
-    uint4 q[NT][kKv];
-    float scale[NT][2], gain[NT][2];
-    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.a.q) + static_cast<int64_t>(b) * p.a.hq * D;
+  // the query rows as B fragments: column g of tile n is head h0 + 8 n + g
+  __device__ __forceinline__ void load_q(const Plan& p, int b, int h0, int nh) {
+    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.a.q) + (static_cast<int64_t>(b) * p.a.hq + h0) * D;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = 8 * n + g;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < kKv; ++c)
-        q[n][c] = col < nh ? load_row16(qp + static_cast<int64_t>(h0 + col) * D + t * 8 + c * 32) : zero;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = 8 * n + 2 * t + e;
-        scale[n][e] = h < nh ? 1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h0 + h]) : 0.0f;
-        gain[n][e] = h < nh ? p.a.gain[h0 + h] : 0.0f;
-      }
-    }
-    float m[NT][2], l[NT][2], o[NT][D / 16][4];
+        q[n][c] = 8 * n + g() < nh ? load_row16(qp + (8 * n + g()) * D + t() * 8 + c * 32) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void begin(const Plan& p, int h0, int nh) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        const int h = 8 * n + 2 * t() + e;
+        scale[n][e] = h < nh ? 1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h0 + h]) : 0.0f;
+        gain[n][e] = h < nh ? p.a.gain[h0 + h] : 0.0f;
         m[n][e] = -INFINITY;
         l[n][e] = 0.0f;
       }
@@ -189,83 +164,113 @@ struct CoreBf16 {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
     }
-
-    for (int key = key0 + warp * 16; key < key_end; key += kTile) {
-      const Keys next = locate(p, b, hk, min(len, key_end), key + kTile, bad);
-      float s[NT][4];
+  }
+  __device__ __forceinline__ void load_k(const Plan& p, const Keys (&keys)[R], int) {
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const Keys& at = keys[x];
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.k_pages) + (at.row + g()) * D + t() * 8;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool in = g() + 8 * r < at.n;
+#pragma unroll
+        for (int c = 0; c < kKv; ++c) k[x][r][c] = in ? load_row16(src + 8 * r * D + c * 32) : make_uint4(0u, 0u, 0u, 0u);
+        gate[x][r] = !in ? -INFINITY : p.a.logsig_pages ? p.a.logsig_pages[at.gate + g() + 8 * r] : 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void load_v(const Plan& p, const Keys (&keys)[R], int) {
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const Keys& at = keys[x];
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.v_pages) + (at.row + 2 * t()) * D + g() * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = (i & 1) + 8 * (i >> 1);
+#pragma unroll
+        for (int c = 0; c < kVv; ++c)
+          v[x][i][c] = 2 * t() + key < at.n ? load_row16(src + key * D + c * 64) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  __device__ __forceinline__ void scores() {
+    bool over = false;
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      // a token whose log-gate is -inf has no weight whatever its k holds
+      const bool out0 = gate[x][0] == -INFINITY, out1 = gate[x][1] == -INFINITY;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+        float a[4] = {}, b[4] = {};  // two chains of products
 #pragma unroll
         for (int c = 0; c < kKv; ++c) {
-          mma16816(s[n], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, q[n][c].x, q[n][c].y);
-          mma16816(s[n], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, q[n][c].z, q[n][c].w);
+          mma16816(a, k[x][0][c].x, k[x][1][c].x, k[x][0][c].y, k[x][1][c].y, q[n][c].x, q[n][c].y);
+          mma16816(b, k[x][0][c].z, k[x][1][c].z, k[x][0][c].w, k[x][1][c].w, q[n][c].z, q[n][c].w);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[x][n][e] = out0 ? -INFINITY : fmaf(a[e] + b[e], scale[n][e], gain[n][e] * gate[x][0]);
+          s[x][n][2 + e] = out1 ? -INFINITY : fmaf(a[2 + e] + b[2 + e], scale[n][e], gain[n][e] * gate[x][1]);
+          over |= fmaxf(s[x][n][e], s[x][n][2 + e]) > m[n][e] + kSlack;
         }
       }
-      const float gate0 = gate[0], gate1 = gate[1];
-      load_k(next);
-      // a token whose log-gate is -inf has no weight whatever its v holds: 0 x NaN must not reach the sums
-      const bool out0 = gate0 == -INFINITY, out1 = gate1 == -INFINITY;
+      // nor whatever its v holds: 0 x NaN must not reach the sums
       const uint32_t gone0 = __ballot_sync(0xffffffffu, out0), gone1 = __ballot_sync(0xffffffffu, out1);
       if (gone0 | gone1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (((i >> 1 ? gone1 : gone0) >> (4 * (2 * t + (i & 1)))) & 1u)
+          if (((i >> 1 ? gone1 : gone0) >> (4 * (2 * t() + (i & 1)))) & 1u)
 #pragma unroll
-            for (int c = 0; c < kVv; ++c) v[i][c] = zero;
+            for (int c = 0; c < kVv; ++c) v[x][i][c] = make_uint4(0u, 0u, 0u, 0u);
       }
-      bool over = false;
+    }
+    if (__any_sync(0xffffffffu, over)) {  // (a reference of -inf is exceeded by any logit)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          s[n][e] = out0 ? -INFINITY : fmaf(s[n][e], scale[n][e], gain[n][e] * gate0);
-          s[n][2 + e] = out1 ? -INFINITY : fmaf(s[n][2 + e], scale[n][e], gain[n][e] * gate1);
-          over |= fmaxf(s[n][e], s[n][2 + e]) > m[n][e] + kSlack;
-        }
-      if (__any_sync(0xffffffffu, over)) {  // (a reference of -inf is exceeded by any logit)
+          float y = m[n][e];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int x = 0; x < R; ++x) y = fmaxf(y, fmaxf(s[x][n][e], s[x][n][2 + e]));
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(m[n][e], fmaxf(s[n][e], s[n][2 + e]));
+          for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
+          const float c = weight(m[n][e], y);
+          m[n][e] = y;
+          l[n][e] *= c;
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-            const float c = weight(m[n][e], x);
-            m[n][e] = x;
-            l[n][e] *= c;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[n][i][e] *= c;
-              o[n][i][2 + e] *= c;
-            }
+          for (int i = 0; i < D / 16; ++i) {
+            o[n][i][e] *= c;
+            o[n][i][2 + e] *= c;
           }
-      }
-      uint32_t pb[NT][2], pc[NT][2];  // the rounded weights, what they lack
+        }
+    }
+  }
+  __device__ __forceinline__ void accumulate() {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+    for (int x = 0; x < R; ++x) {
+      uint32_t hi[NT][2], lo[NT][2];  // the rounded weights, what they lack
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float w0 = weight(s[n][2 * r], m[n][0]), w1 = weight(s[n][2 * r + 1], m[n][1]);
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(w0, w1);
-          const float2 f = __bfloat1622float2(hi);
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(w0 - f.x, w1 - f.y);
+          const float w0 = weight(s[x][n][2 * r], m[n][0]), w1 = weight(s[x][n][2 * r + 1], m[n][1]);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(w0, w1);
+          const float2 f = __bfloat1622float2(h);
+          const __nv_bfloat162 rest = __floats2bfloat162_rn(w0 - f.x, w1 - f.y);
           l[n][0] += w0;
           l[n][1] += w1;
           uint32_t bits;
-          memcpy(&bits, &hi, 4);
-          pb[n][r] = transpose8x8(bits);
-          memcpy(&bits, &lo, 4);
-          pc[n][r] = transpose8x8(bits);
+          memcpy(&bits, &h, 4);
+          hi[n][r] = transpose8x8(bits);
+          memcpy(&bits, &rest, 4);
+          lo[n][r] = transpose8x8(bits);
         }
-      }
 #pragma unroll
       for (int c = 0; c < kVv; ++c) {
-        const uint32_t* v0 = &v[0][c].x;
-        const uint32_t* v1 = &v[1][c].x;
-        const uint32_t* v2 = &v[2][c].x;
-        const uint32_t* v3 = &v[3][c].x;
+        const uint32_t v0[4] = {v[x][0][c].x, v[x][0][c].y, v[x][0][c].z, v[x][0][c].w};
+        const uint32_t v1[4] = {v[x][1][c].x, v[x][1][c].y, v[x][1][c].z, v[x][1][c].w};
+        const uint32_t v2[4] = {v[x][2][c].x, v[x][2][c].y, v[x][2][c].z, v[x][2][c].w};
+        const uint32_t v3[4] = {v[x][3][c].x, v[x][3][c].y, v[x][3][c].z, v[x][3][c].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // rows g and g + 8 of the instruction are columns c * 64 + g * 8 + 2 i and the next
@@ -273,152 +278,150 @@ struct CoreBf16 {
           const uint32_t a2 = __byte_perm(v2[i], v3[i], 0x5410), a3 = __byte_perm(v2[i], v3[i], 0x7632);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816(o[n][c * 4 + i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-            mma16816(o[n][c * 4 + i], a0, a1, a2, a3, pc[n][0], pc[n][1]);
+            mma16816(o[n][c * 4 + i], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+            mma16816(o[n][c * 4 + i], a0, a1, a2, a3, lo[n][0], lo[n][1]);
           }
         }
       }
-      load_v(next);
     }
-
-    // the warp's sums, over the eight lanes of a column
+  }
+  // the warp's sums, over the eight lanes of a column
+  __device__ __forceinline__ void store(int nh, float* part_m, float* part_l, float* part_o) {
+    const int warp = threadIdx.x >> 5;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
-        const int h = 8 * n + 2 * t + e;
+        const int h = 8 * n + 2 * t() + e;
         if (h >= nh) continue;
-        if (g == 0) {
+        if (g() == 0) {
           part_m[warp * kHeads + h] = m[n][e];
           part_l[warp * kHeads + h] = l[n][e];
         }
-        float* dst = part_o + (warp * kHeads + h) * D + g * 8;
+        float* dst = part_o + (warp * kHeads + h) * D + g() * 8;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          dst[(i >> 2) * 64 + 2 * (i & 3)] = o[n][i][e];
-          dst[(i >> 2) * 64 + 2 * (i & 3) + 1] = o[n][i][2 + e];
-        }
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float2*>(dst + (i >> 2) * 64 + 2 * (i & 3)) = make_float2(o[n][i][e], o[n][i][2 + e]);
       }
   }
 };
 
-// ---- fp32: eight lanes to a key, each with D / 8 of its columns ----------------------------------
+// ---- fp32: 4 R keys at a time, eight lanes to a key, each with D / 8 of its columns --------------
 template <int D, int NH>
 struct CoreFp32 {
   static constexpr int kHeads = NH;
+  static constexpr int R = 256 / D;  // keys per lane
+  static constexpr int kKeys = 16;
+  static constexpr int kSteps = 4 / R;
   static constexpr int kVec = D / 32;  // 16-byte pieces per lane and row
-  static constexpr int kMinCtas = ctas_per_sm(false, NH, D);
 
+  float4 q[NH][kVec], k[R][kVec], v[R][kVec], o[NH][kVec];
+  float gate[R], scale[NH], gain[NH], m[NH], l[NH], s[NH][R];
+
+  static __device__ __forceinline__ int sub() { return threadIdx.x & 7; }          // the lane's columns
+  static __device__ __forceinline__ int kg() { return (threadIdx.x & 31) >> 3; }   // its key of four
   static __device__ __forceinline__ float4 load4(const float* p) {
     const uint4 x = load_row16(p);
     return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
   }
+  static __device__ __forceinline__ float4 zero() { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
 
-  static __device__ __forceinline__ void run(const Plan& p, int b, int hk, int h0, int nh, int key0, int key_end,
-                                             int len, float* part_m, float* part_l, float* part_o, bool* bad) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & 7, kg = lane >> 3;  // the lane's columns; its key of four
-    const float* kp = static_cast<const float*>(p.a.k_pages);
-    const float* vp = static_cast<const float*>(p.a.v_pages);
-    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float4 k[2][kVec], v[2][kVec];
-    float gate[2];
-    // a step is 8 keys: half of the warp's 16, keys kg and kg + 4 of it on this lane
-    auto load_k = [&](const Keys& s, int half) {
+  __device__ __forceinline__ void load_q(const Plan& p, int b, int h0, int nh) {
+    const float* qp = static_cast<const float*>(p.a.q) + (static_cast<int64_t>(b) * p.a.hq + h0) * D + sub() * 4;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int key = half * 8 + r * 4 + kg;
-        const bool in = key < s.n;
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) k[r][c] = in ? load4(kp + (s.row + key) * D + sub * 4 + c * 32) : zero;
-        gate[r] = !in ? -INFINITY : p.a.logsig_pages ? p.a.logsig_pages[s.gate + key] : 0.0f;
-      }
-    };
-    auto load_v = [&](const Keys& s, int half) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int key = half * 8 + r * 4 + kg;
-#pragma unroll
-        for (int c = 0; c < kVec; ++c)
-          v[r][c] = key < s.n ? load4(vp + (s.row + key) * D + sub * 4 + c * 32) : zero;
-      }
-    };
-    Keys at = locate(p, b, hk, min(len, key_end), key0 + warp * 16, bad);
-    load_k(at, 0);
-    load_v(at, 0);
-    float4 q[NH][kVec], o[NH][kVec];
-    float scale[NH], gain[NH], m[NH], l[NH];
-    const float* qp = static_cast<const float*>(p.a.q) + (static_cast<int64_t>(b) * p.a.hq + h0) * D;
+      for (int c = 0; c < kVec; ++c) q[h][c] = h < nh ? load4(qp + h * D + c * 32) : zero();
+  }
+  __device__ __forceinline__ void begin(const Plan& p, int h0, int nh) {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-#pragma unroll
-      for (int c = 0; c < kVec; ++c) {
-        q[h][c] = h < nh ? load4(qp + h * D + sub * 4 + c * 32) : zero;
-        o[h][c] = zero;
-      }
       scale[h] = h < nh ? 1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h0 + h]) : 0.0f;
       gain[h] = h < nh ? p.a.gain[h0 + h] : 0.0f;
       m[h] = -INFINITY;
       l[h] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) o[h][c] = zero();
     }
-    for (int key = key0 + warp * 16; key < key_end; key += kTile) {
-      const Keys next = locate(p, b, hk, min(len, key_end), key + kTile, bad);
+  }
+  // one step of the warp's 16 keys: keys kg, kg + 4, ... of its 4 R on this lane
+  __device__ __forceinline__ void load_k(const Plan& p, const Keys (&keys)[1], int step) {
+    const Keys& at = keys[0];
+    const float* src = static_cast<const float*>(p.a.k_pages) + (at.row + step * 4 * R + kg()) * D + sub() * 4;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float s[NH][2];
-        bool over = false;
+    for (int r = 0; r < R; ++r) {
+      const int key = step * 4 * R + r * 4 + kg();
+      const bool in = key < at.n;
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
+      for (int c = 0; c < kVec; ++c) k[r][c] = in ? load4(src + r * 4 * D + c * 32) : zero();
+      gate[r] = !in ? -INFINITY : p.a.logsig_pages ? p.a.logsig_pages[at.gate + key] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void load_v(const Plan& p, const Keys (&keys)[1], int step) {
+    const Keys& at = keys[0];
+    const float* src = static_cast<const float*>(p.a.v_pages) + (at.row + step * 4 * R + kg()) * D + sub() * 4;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float x = 0.0f;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int c = 0; c < kVec; ++c)
-              x = fmaf(q[h][c].x, k[r][c].x, fmaf(q[h][c].y, k[r][c].y, fmaf(q[h][c].z, k[r][c].z, fmaf(q[h][c].w, k[r][c].w, x))));
+      for (int c = 0; c < kVec; ++c)
+        v[r][c] = step * 4 * R + r * 4 + kg() < at.n ? load4(src + r * 4 * D + c * 32) : zero();
+  }
+  __device__ __forceinline__ void scores() {
+    bool over = false;
 #pragma unroll
-            for (int w = 1; w < 8; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-            s[h][r] = gate[r] == -INFINITY ? -INFINITY : fmaf(x, scale[h], gain[h] * gate[r]);
-            over |= s[h][r] > m[h] + kSlack;
-          }
-        const bool out[2] = {gate[0] == -INFINITY, gate[1] == -INFINITY};
-        load_k(half == 0 ? at : next, half ^ 1);
-        if (__any_sync(0xffffffffu, over)) {
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const float x = fmaxf(m[h], fmaxf(s[h][0], s[h][1]));
-            const float c = weight(m[h], x);
-            m[h] = x;
-            l[h] *= c;
+      for (int r = 0; r < R; ++r) {
+        float x = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i)
-              o[h][i] = make_float4(o[h][i].x * c, o[h][i].y * c, o[h][i].z * c, o[h][i].w * c);
-          }
-        }
+        for (int c = 0; c < kVec; ++c)
+          x = fmaf(q[h][c].x, k[r][c].x,
+                   fmaf(q[h][c].y, k[r][c].y, fmaf(q[h][c].z, k[r][c].z, fmaf(q[h][c].w, k[r][c].w, x))));
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (out[r])
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) v[r][c] = zero;  // 0 x NaN must not reach the sums
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const float w = weight(s[h][r], m[h]);
-            l[h] += w;
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-              o[h][c].x = fmaf(w, v[r][c].x, o[h][c].x);
-              o[h][c].y = fmaf(w, v[r][c].y, o[h][c].y);
-              o[h][c].z = fmaf(w, v[r][c].z, o[h][c].z);
-              o[h][c].w = fmaf(w, v[r][c].w, o[h][c].w);
-            }
-          }
-        }
-        load_v(half == 0 ? at : next, half ^ 1);
+        for (int w = 1; w < 8; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
+        s[h][r] = gate[r] == -INFINITY ? -INFINITY : fmaf(x, scale[h], gain[h] * gate[r]);
+        over |= s[h][r] > m[h] + kSlack;
       }
-      at = next;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (gate[r] == -INFINITY)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) v[r][c] = zero();  // 0 x NaN must not reach the sums
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float x = m[h];
+#pragma unroll
+        for (int r = 0; r < R; ++r) x = fmaxf(x, s[h][r]);
+        const float c = weight(m[h], x);
+        m[h] = x;
+        l[h] *= c;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) o[h][i] = make_float4(o[h][i].x * c, o[h][i].y * c, o[h][i].z * c, o[h][i].w * c);
+      }
     }
-    // join the four keys' sums of the warp
+  }
+  __device__ __forceinline__ void accumulate() {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const float w = weight(s[h][r], m[h]);
+        l[h] += w;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+          o[h][c].x = fmaf(w, v[r][c].x, o[h][c].x);
+          o[h][c].y = fmaf(w, v[r][c].y, o[h][c].y);
+          o[h][c].z = fmaf(w, v[r][c].z, o[h][c].z);
+          o[h][c].w = fmaf(w, v[r][c].w, o[h][c].w);
+        }
+      }
+  }
+  // the sums of the warp's four keys at a time, joined
+  __device__ __forceinline__ void store(int nh, float* part_m, float* part_l, float* part_o) {
+    const int warp = threadIdx.x >> 5;
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       float x = m[h];
@@ -438,9 +441,9 @@ struct CoreFp32 {
           y.z += __shfl_xor_sync(0xffffffffu, y.z, w);
           y.w += __shfl_xor_sync(0xffffffffu, y.w, w);
         }
-        if (h < nh && kg == 0) *reinterpret_cast<float4*>(part_o + (warp * NH + h) * D + sub * 4 + i * 32) = y;
+        if (h < nh && kg() == 0) *reinterpret_cast<float4*>(part_o + (warp * NH + h) * D + sub() * 4 + i * 32) = y;
       }
-      if (h < nh && lane == 0) {
+      if (h < nh && (threadIdx.x & 31) == 0) {
         part_m[warp * NH + h] = x;
         part_l[warp * NH + h] = sum;
       }
@@ -451,23 +454,23 @@ struct CoreFp32 {
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-__device__ __forceinline__ int checked_length(const Plan& p, int b, bool* bad) {
-  const int64_t most = static_cast<int64_t>(p.a.max_pages) << p.a.page_shift;
-  const int len = p.a.lens[b];
-  if (len >= 0 && len <= most) return len;
-  *bad = true;
-  return len < 0 ? 0 : static_cast<int>(most);
-}
+// A place in the list of tiles: tile j of unit u of sequence b.
+struct Place {
+  int32_t b, u, j, tiles;  // tiles of every unit of the sequence
+};
 
 template <typename T, int D, typename Core>
-__global__ void __launch_bounds__(kThreads, Core::kMinCtas) paged_attn_kernel(const __grid_constant__ Plan p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kHeads, D))
+    paged_attn_kernel(const __grid_constant__ Plan p) {
   constexpr int H = Core::kHeads;
+  constexpr int kGroups = Core::kKeys / 16;      // groups of 16 keys of a warp
+  constexpr int kTile = Core::kKeys * kWarps;
   constexpr int kSlot = H * (D + 2);  // floats of a partial sum: [H][D], then the maxima and the sums
   __shared__ int ends[kMaxSeqs];      // inclusive scan of the sequences' tiles (per unit)
+  __shared__ int lens[kMaxSeqs];
   __shared__ int warp_sums[kWarps];
   __shared__ float part_m[kWarps * H], part_l[kWarps * H];
   __shared__ __align__(16) float part_o[kWarps * H * D];
-  __shared__ bool last_to_arrive;
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -476,11 +479,18 @@ __global__ void __launch_bounds__(kThreads, Core::kMinCtas) paged_attn_kernel(co
   // tiles of every sequence, scanned: a run of sequences per thread
   const int batch = p.a.batch;
   const int run = (batch + kThreads - 1) / kThreads;
+  const int64_t most = static_cast<int64_t>(p.a.max_pages) << p.a.page_shift;
   int sum = 0;
   for (int i = 0; i < run; ++i) {
     const int b = tid * run + i;
     if (b >= batch) break;
-    sum += (checked_length(p, b, &bad) + kTile - 1) / kTile;
+    int len = p.a.lens[b];
+    if (len < 0 || len > most) {
+      bad = true;
+      len = len < 0 ? 0 : static_cast<int>(most);
+    }
+    lens[b] = len;
+    sum += (len + kTile - 1) / kTile;
     ends[b] = sum;
   }
   int scan = sum;
@@ -499,10 +509,29 @@ __global__ void __launch_bounds__(kThreads, Core::kMinCtas) paged_attn_kernel(co
     ends[b] += before;
   }
   __syncthreads();
-  const int64_t total = static_cast<int64_t>(ends[batch - 1]) * p.units;
-  const int64_t per = p.counters ? (total + gridDim.x - 1) / gridDim.x : 0;
 
-  // the join of kWarps partial sums in shared memory into `out`, or into a slot for the unit's last CTA
+  // this CTA's run of the list: an equal share with a workspace, whole units without
+  const int64_t total = static_cast<int64_t>(ends[batch - 1]) * p.units;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  int64_t at = min(total, per * blockIdx.x), end = min(total, at + per);
+  if (!p.shares) {
+    const int64_t units = static_cast<int64_t>(batch) * p.units, share = (units + gridDim.x - 1) / gridDim.x;
+    auto offset = [&](int64_t unit) {
+      if (unit >= units) return total;
+      const int b = static_cast<int>(unit / p.units), first = b > 0 ? ends[b - 1] : 0;
+      return static_cast<int64_t>(first) * p.units + (unit - static_cast<int64_t>(b) * p.units) * (ends[b] - first);
+    };
+    at = offset(share * blockIdx.x);
+    end = offset(share * (blockIdx.x + 1));
+  }
+
+  auto heads_of = [&](int u, int* hk, int* h0, int* nh) {
+    *hk = u / p.blocks;
+    const int block = u - *hk * p.blocks;
+    *h0 = *hk * p.group + block * H;
+    *nh = min(H, p.group - block * H);
+  };
+  // The join of kWarps sums in shared memory, into the output or into a slot for the second kernel.
   auto finish = [&](int b, int h0, int nh, float* slot) {
     __syncthreads();
     for (int i = tid; i < nh * D; i += kThreads) {
@@ -528,125 +557,182 @@ __global__ void __launch_bounds__(kThreads, Core::kMinCtas) paged_attn_kernel(co
         if (d == 0 && p.a.lse) p.a.lse[static_cast<int64_t>(h0 + h) * batch + b] = l == 0.0f ? -INFINITY : top + logf(l);
       }
     }
-  };
-  auto heads_of = [&](int u, int* hk, int* h0, int* nh) {
-    *hk = u / p.blocks;
-    const int block = u - *hk * p.blocks;
-    *h0 = *hk * p.group + block * H;
-    *nh = min(H, p.group - block * H);
+    __syncthreads();
   };
 
-  int64_t at = per * blockIdx.x;
-  const int64_t end = min(total, at + per);
-  int b = 0;
+  auto find = [&](int b, int hk, int tile, Keys (&keys)[kGroups]) {
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x)
+      keys[x] = locate(p, b, hk, lens[b], tile * kTile + (warp * kGroups + x) * 16, &bad);
+  };
   if (at < end) {
-    int hi = batch - 1;  // the first sequence whose tiles reach past `at`
-    while (b < hi) {
-      const int mid = (b + hi) >> 1;
-      if (static_cast<int64_t>(ends[mid]) * p.units > at) hi = mid;
-      else b = mid + 1;
-    }
-  }
-  while (at < end) {
-    const int first = b > 0 ? ends[b - 1] : 0, tiles = ends[b] - first;
-    if (tiles == 0) {
-      ++b;
-      continue;
-    }
-    const int64_t in_seq = at - static_cast<int64_t>(first) * p.units;
-    const int u = static_cast<int>(in_seq / tiles), j0 = static_cast<int>(in_seq - static_cast<int64_t>(u) * tiles);
-    const int n = static_cast<int>(min(static_cast<int64_t>(tiles - j0), end - at));
-    int hk, h0, nh;
-    heads_of(u, &hk, &h0, &nh);
-    const int len = checked_length(p, b, &bad);
-    Core::run(p, b, hk, h0, nh, j0 * kTile, (j0 + n) * kTile, len, part_m, part_l, part_o, &bad);
-    if (n == tiles) {
-      finish(b, h0, nh, nullptr);
-    } else {
-      // slot 2c + 1: the unit begins in CTA c; slot 2c: it began before
-      const int64_t begin = at - j0;
-      const int c0 = static_cast<int>(begin / per), c1 = static_cast<int>((begin + tiles - 1) / per);
-      finish(b, h0, nh, p.partial + static_cast<int64_t>(2 * blockIdx.x + (j0 == 0)) * kSlot);
-      __threadfence();
-      __syncthreads();
-      int* counter = p.counters + static_cast<int64_t>(b) * p.units + u;
-      if (tid == 0) last_to_arrive = atomicAdd(counter, 1) == c1 - c0;
-      __syncthreads();
-      if (last_to_arrive) {
-        __threadfence();
-        if (tid == 0) *counter = 0;  // for the next call
-        // a warp joins every kWarps-th part, four at a time
-        for (int h = 0; h < nh; ++h) {
-          constexpr int kPer = D / 32;
-          float m = -INFINITY, l = 0.0f, o[kPer] = {};
-          for (int c = c0 + warp; c <= c1; c += 4 * kWarps) {
-            float pm[4], pl[4], po[4][kPer];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int cc = c + x * kWarps;
-              const float* s = p.partial + static_cast<int64_t>(2 * cc + (cc == c0)) * kSlot;
-              pm[x] = cc <= c1 ? __ldcg(s + H * D + h) : -INFINITY;
-              pl[x] = cc <= c1 ? __ldcg(s + H * D + H + h) : 0.0f;
-#pragma unroll
-              for (int e = 0; e < kPer; ++e) po[x][e] = cc <= c1 ? __ldcg(s + h * D + lane + 32 * e) : 0.0f;
-            }
-            const float top = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
-            const float c_old = weight(m, top);
-            m = top;
-            l *= c_old;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) o[e] *= c_old;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float w = weight(pm[x], top);
-              l = fmaf(pl[x], w, l);
-#pragma unroll
-              for (int e = 0; e < kPer; ++e) o[e] = fmaf(po[x][e], w, o[e]);
-            }
-          }
-          if (lane == 0) {
-            part_m[warp * H + h] = m;
-            part_l[warp * H + h] = l;
-          }
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) part_o[(warp * H + h) * D + lane + 32 * e] = o[e];
-        }
-        finish(b, h0, nh, nullptr);
+    Place now;
+    {
+      int lo = 0, hi = batch - 1;  // the first sequence whose tiles reach past `at`
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int64_t>(ends[mid]) * p.units > at) hi = mid;
+        else lo = mid + 1;
       }
+      const int first = lo > 0 ? ends[lo - 1] : 0;
+      const int64_t in_seq = at - static_cast<int64_t>(first) * p.units;
+      now.b = lo;
+      now.tiles = ends[lo] - first;
+      now.u = static_cast<int>(in_seq / now.tiles);
+      now.j = static_cast<int>(in_seq - static_cast<int64_t>(now.u) * now.tiles);
     }
-    __syncthreads();  // the next segment writes the partial sums in shared memory
-    at += n;
-    if (j0 + n == tiles && u == p.units - 1) ++b;
+    int hk, h0, nh;
+    heads_of(now.u, &hk, &h0, &nh);
+    Core core;
+    Keys keys[kGroups];
+    find(now.b, hk, now.j, keys);
+    core.load_k(p, keys, 0);
+    core.load_v(p, keys, 0);
+    core.load_q(p, now.b, h0, nh);
+    core.begin(p, h0, nh);
+    int j0 = now.j;  // where the present unit was entered
+    for (;; ++at) {
+      // the next tile, whose rows are requested before this one's are used up
+      Place next = now;
+      const bool more = at + 1 < end;
+      bool turn = !more;
+      int next_hk = hk, next_h0 = h0, next_nh = nh;
+      Keys next_keys[kGroups] = {};
+      if (more) {
+        if (++next.j == next.tiles) {
+          turn = true;
+          next.j = 0;
+          if (++next.u == p.units) {
+            next.u = 0;
+            do {
+              ++next.b;
+              next.tiles = ends[next.b] - ends[next.b - 1];
+            } while (next.tiles == 0);
+          }
+          heads_of(next.u, &next_hk, &next_h0, &next_nh);
+        }
+        find(next.b, next_hk, next.j, next_keys);
+      }
+#pragma unroll
+      for (int step = 0; step < Core::kSteps; ++step) {
+        const bool through = step == Core::kSteps - 1;
+        core.scores();
+        core.load_k(p, through ? next_keys : keys, through ? 0 : step + 1);
+        if (through && turn && more) core.load_q(p, next.b, next_h0, next_nh);
+        core.accumulate();
+        core.load_v(p, through ? next_keys : keys, through ? 0 : step + 1);
+      }
+      if (turn) {
+        core.store(nh, part_m, part_l, part_o);
+        // slot 2c + 1: the unit begins in CTA c; slot 2c: it began before
+        const bool whole = j0 == 0 && now.j == now.tiles - 1;
+        finish(now.b, h0, nh, whole ? nullptr : p.partial + static_cast<int64_t>(2 * blockIdx.x + (j0 == 0)) * kSlot);
+        if (j0 == 0 && p.shares && tid == 0) {
+          const int64_t last = at - now.j + now.tiles - 1;  // the unit's last tile
+          p.shares[static_cast<int64_t>(now.b) * p.units + now.u] =
+              whole ? make_int2(0, -1) : make_int2(blockIdx.x, static_cast<int>(last / per));
+        }
+        if (!more) break;
+        core.begin(p, next_h0, next_nh);
+        j0 = 0;
+      }
+      now = next;
+#pragma unroll
+      for (int x = 0; x < kGroups; ++x) keys[x] = next_keys[x];
+      hk = next_hk;
+      h0 = next_h0;
+      nh = next_nh;
+    }
   }
 
-  // without a workspace: whole units, one after another
-  if (!p.counters) {
-    const int64_t units = static_cast<int64_t>(batch) * p.units;
-    for (int64_t i = blockIdx.x; i < units; i += gridDim.x) {
-      const int bb = static_cast<int>(i / p.units);
-      int hk, h0, nh;
-      heads_of(static_cast<int>(i - static_cast<int64_t>(bb) * p.units), &hk, &h0, &nh);
-      const int len = checked_length(p, bb, &bad);
-      if (len == 0) continue;
-      Core::run(p, bb, hk, h0, nh, 0, (len + kTile - 1) / kTile * kTile, len, part_m, part_l, part_o, &bad);
-      finish(bb, h0, nh, nullptr);
-      __syncthreads();
-    }
-  }
   // sequences without tokens are in no run
   for (int i = blockIdx.x; i < batch; i += gridDim.x) {
-    if (checked_length(p, i, &bad) != 0) continue;
+    if (lens[i] != 0) continue;
     for (int x = tid; x < p.a.hq * D; x += kThreads)
       put(static_cast<T*>(p.a.out) + static_cast<int64_t>(i) * p.a.hq * D + x, 0.0f);
     if (p.a.lse)
       for (int h = tid; h < p.a.hq; h += kThreads) p.a.lse[static_cast<int64_t>(h) * batch + i] = -INFINITY;
+    if (p.shares)
+      for (int u = tid; u < p.units; u += kThreads) p.shares[static_cast<int64_t>(i) * p.units + u] = make_int2(0, -1);
   }
   if (bad) atomicOr(p.a.status, kDevPageIndex);
 }
 
+// The parts of one head of a shared unit, joined in order: a warp takes every kWarps-th part, four
+// at a time, a lane D / 32 columns of them; then the warps' sums.
+constexpr int kJoinThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Plan p, int heads) {
+  constexpr int kJoinWarps = kJoinThreads / 32;
+  constexpr int kPer = D / 32;
+  __shared__ float part_m[kJoinWarps], part_l[kJoinWarps], part_o[kJoinWarps][D];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t unit = blockIdx.x;
+  const int2 share = p.shares[unit];
+  if (share.y < share.x) return;
+  const int b = static_cast<int>(unit / p.units), u = static_cast<int>(unit - static_cast<int64_t>(b) * p.units);
+  const int hk = u / p.blocks, block = u - hk * p.blocks, h = blockIdx.y;
+  if (h >= p.group - block * heads) return;
+  const int64_t slot = static_cast<int64_t>(heads) * (D + 2);
+  float m = -INFINITY, l = 0.0f, o[kPer] = {};
+  for (int c = share.x + warp; c <= share.y; c += 4 * kJoinWarps) {
+    float pm[4], pl[4], po[4][kPer];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int cc = c + x * kJoinWarps;
+      const float* part = p.partial + (2 * cc + (cc == share.x)) * slot;
+      pm[x] = cc <= share.y ? part[heads * D + h] : -INFINITY;
+      pl[x] = cc <= share.y ? part[heads * D + heads + h] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) po[x][e] = cc <= share.y ? part[h * D + lane + 32 * e] : 0.0f;
+    }
+    const float top = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
+    const float c_old = weight(m, top);
+    m = top;
+    l *= c_old;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] *= c_old;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float w = weight(pm[x], top);
+      l = fmaf(pl[x], w, l);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = fmaf(po[x][e], w, o[e]);
+    }
+  }
+  if (lane == 0) {
+    part_m[warp] = m;
+    part_l[warp] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) part_o[warp][lane + 32 * e] = o[e];
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  float top = -INFINITY, sum = 0.0f, x = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, part_m[w]);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float c = weight(part_m[w], top);
+    sum = fmaf(part_l[w], c, sum);
+    x = fmaf(part_o[w][d], c, x);
+  }
+  const int head = hk * p.group + block * heads + h;
+  put(static_cast<T*>(p.a.out) + (static_cast<int64_t>(b) * p.a.hq + head) * D + d, sum == 0.0f ? 0.0f : x / sum);
+  if (d == 0 && p.a.lse)
+    p.a.lse[static_cast<int64_t>(head) * p.a.batch + b] = sum == 0.0f ? -INFINITY : top + logf(sum);
+}
+
 template <typename T, int D, typename Core>
 cudaError_t launch_core(const Plan& p, int grid, cudaStream_t st) {
-  return launch_pdl(paged_attn_kernel<T, D, Core>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, p);
+  const cudaError_t e = launch_pdl(paged_attn_kernel<T, D, Core>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, p);
+  if (e != cudaSuccess || !p.shares) return e;
+  const dim3 join(static_cast<unsigned>(static_cast<int64_t>(p.a.batch) * p.units),
+                  static_cast<unsigned>(Core::kHeads < p.group ? Core::kHeads : p.group));
+  return launch_pdl(paged_join_kernel<T, D>, join, dim3(kJoinThreads), 0, st, p, Core::kHeads);
 }
 
 template <int D>
@@ -661,7 +747,7 @@ cudaError_t launch_dim(const Plan& p, bool bf16, int heads, int grid, cudaStream
 
 struct Shape {
   int group, heads, blocks, units, grid;
-  size_t counter_bytes, slot_bytes;
+  size_t share_bytes, slot_bytes;
 };
 
 Shape shape_of(bool bf16, int batch, int hq, int hkv, int head_dim) {
@@ -671,7 +757,7 @@ Shape shape_of(bool bf16, int batch, int hq, int hkv, int head_dim) {
   s.blocks = (s.group + s.heads - 1) / s.heads;
   s.units = hkv * s.blocks;
   s.grid = num_sms() * ctas_per_sm(bf16, s.heads, head_dim);
-  s.counter_bytes = (static_cast<size_t>(batch) * s.units * sizeof(int32_t) + 255) / 256 * 256;
+  s.share_bytes = (static_cast<size_t>(batch) * s.units * sizeof(int2) + 255) / 256 * 256;
   s.slot_bytes = sizeof(float) * s.heads * (head_dim + 2);
   return s;
 }
@@ -680,7 +766,7 @@ Shape shape_of(bool bf16, int batch, int hq, int hkv, int head_dim) {
 
 size_t paged_attention_workspace_bytes(tg_dtype dt, int batch, int hq, int hkv, int head_dim) {
   const Shape s = shape_of(dt == TG_BF16, batch, hq, hkv, head_dim);
-  return s.counter_bytes + 2 * s.grid * s.slot_bytes;
+  return s.share_bytes + 2 * s.grid * s.slot_bytes;
 }
 
 tg_status launch_paged_attention(const PagedAttnArgs& a, tg_dtype dt, int head_dim, void* workspace,
@@ -692,8 +778,8 @@ tg_status launch_paged_attention(const PagedAttnArgs& a, tg_dtype dt, int head_d
   p.group = s.group;
   p.blocks = s.blocks;
   p.units = s.units;
-  p.counters = static_cast<int32_t*>(workspace);
-  p.partial = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + s.counter_bytes) : nullptr;
+  p.shares = static_cast<int2*>(workspace);
+  p.partial = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + s.share_bytes) : nullptr;
   return cuda_check(head_dim == 128 ? launch_dim<128>(p, bf16, s.heads, s.grid, st)
                                     : launch_dim<64>(p, bf16, s.heads, s.grid, st),
                     "paged attention launch");
