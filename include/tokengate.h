@@ -566,7 +566,7 @@ TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int3
  *         order; without it one SM reads them all.  16-byte aligned, any
  *         contents.  TG_ERR_WORKSPACE when smaller.  Calls that share a workspace
  *         must not overlap on the GPU.
- *   head_dim 64 or 128, 16-byte aligned q, k_pages, v_pages and out.
+ *   head_dim 64 or 128, n_q_heads <= 512; q, k_pages, v_pages and out 16-byte aligned.
  */
 TG_API tg_status tg_paged_attention(const void* q, const void* k_pages, const void* v_pages,
                                     tg_dtype dtype, int32_t batch, int32_t n_q_heads,

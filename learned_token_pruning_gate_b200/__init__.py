@@ -187,20 +187,7 @@ def _ptr(t):
 
 
 def _stream(device=None):
-    """The raw handle of the current stream (of the tensors' device)."""
-    if device is not None and device.index is not None:
-        return torch._C._cuda_getCurrentRawStream(device.index)  # without a Stream object: 2 us less
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes `device` current for a call; nothing to do when it is already."""
-    if torch.cuda.current_device() == device.index:
-        return _SAME_DEVICE
-    return torch.cuda.device(device)
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
 def _host_i32(a):
@@ -713,6 +700,34 @@ def gated_prefill(h, q, k, v, W1, b1, w2, b2, gain, temp, cu_seqlens, doc_begin,
 
 
 # ---- decoding ----------------------------------------------------------------------------------
+#
+# A decoding step is a few microseconds on the GPU, so its calls look their operands over in one
+# expression (_fits) and go through the checks that name a mismatch (_expect) only when it fails.
+
+
+def _fits(t, shape, dtype, index):
+    """What _expect asks of a tensor, on CUDA device `index`."""
+    return (t.shape == shape and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(index):
+    """Makes CUDA device `index` current for a call; nothing to do when it is already."""
+    if torch.cuda.current_device() == index:
+        return _SAME_DEVICE
+    return torch.cuda.device(index)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _raw_stream(index):
+    """The current stream's handle, without the Stream object that _stream makes (2 us)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _workspace(workspace, device):
@@ -721,7 +736,7 @@ def _workspace(workspace, device):
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
 
 
-def _pools(k_pages, v_pages, logsig_pages):
+def _expect_pools(k_pages, v_pages, logsig_pages):
     """(n_pages, n_kv_heads, page_size, head_dim) of one layer's pages."""
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be [n_pages, n_kv_heads, page_size, head_dim]")
@@ -729,17 +744,13 @@ def _pools(k_pages, v_pages, logsig_pages):
     _expect("k_pages", k_pages, (P, Hkv, page, d), k_pages.dtype, k_pages.device)
     _expect("v_pages", v_pages, (P, Hkv, page, d), k_pages.dtype, k_pages.device)
     _expect("logsig_pages", logsig_pages, (P, page), torch.float32, k_pages.device)
-    return P, Hkv, page, d
 
 
-def _table(table, lens, device):
-    """(batch, max_pages) of a page table and its lengths."""
+def _expect_table(table, lens, device):
     if table.dim() != 2:
         raise ValueError("table must be [batch, max_pages]")
-    B, mp = table.shape
-    _expect("table", table, (B, mp), torch.int32, device)
-    _expect("lens", lens, (B,), torch.int32, device)
-    return B, mp
+    _expect("table", table, table.shape, torch.int32, device)
+    _expect("lens", lens, (table.shape[0],), torch.int32, device)
 
 
 def paged_attention_workspace(batch, n_q_heads, n_kv_heads, head_dim, dtype=torch.bfloat16,
@@ -755,50 +766,88 @@ def paged_attention_workspace(batch, n_q_heads, n_kv_heads, head_dim, dtype=torc
         return torch.empty(int(out.value), dtype=torch.uint8, device=device)
 
 
+def _expect_paged_attention(q, k_pages, v_pages, table, lens, logsig_pages, gain, temp, out, lse):
+    if q.dim() != 3:
+        raise ValueError("q must be [batch, heads, head_dim]")
+    B, Hq, dh = q.shape
+    _expect("q", q, (B, Hq, dh), q.dtype, q.device)
+    _expect_pools(k_pages, v_pages, logsig_pages)
+    Hkv = k_pages.shape[1]
+    if k_pages.shape[3] != dh or k_pages.dtype != q.dtype or k_pages.device != q.device:
+        raise ValueError(f"k_pages: {tuple(k_pages.shape)} {k_pages.dtype} on {k_pages.device} "
+                         f"for q {tuple(q.shape)} {q.dtype} on {q.device}")
+    if Hkv <= 0 or Hq % Hkv != 0:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} kv heads")
+    _expect_table(table, lens, q.device)
+    if table.shape[0] != B:
+        raise ValueError(f"table: {table.shape[0]} sequences, q has {B}")
+    _expect("gain", gain, (Hq,), torch.float32, q.device)
+    _expect("temp", temp, (Hq,), torch.float32, q.device)
+    _expect("out", out, (B, Hq, dh), q.dtype, q.device)
+    _expect("lse", lse, (Hq, B), torch.float32, q.device)
+    _need_cuda(q)
+
+
 def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=None, temp=None,
                     out=None, lse=None, want_lse=False, workspace="auto"):
     """Token-gated attention of one new token per sequence over a paged cache.
 
     q [B, Hq, d]; k_pages, v_pages [P, Hkv, page, d]; table [B, max_pages] and lens [B] int32 on
     the device; logsig_pages [P, page] or None (no bias); gain (None: 1), temp (None: 1) [Hq].
-    workspace: "auto" (allocate one), None (no split), or paged_attention_workspace(...),
-    which a decoding loop keeps.  Returns (out [B, Hq, d], lse [Hq, B] or None)."""
-    if q.dim() != 3:
-        raise ValueError("q must be [batch, heads, head_dim]")
-    B, Hq, dh = q.shape
-    _expect("q", q, (B, Hq, dh), q.dtype, q.device)
-    P, Hkv, page, d = _pools(k_pages, v_pages, logsig_pages)
-    if d != dh or k_pages.dtype != q.dtype or k_pages.device != q.device:
-        raise ValueError(f"k_pages: {tuple(k_pages.shape)} {k_pages.dtype} on {k_pages.device} "
-                         f"for q {tuple(q.shape)} {q.dtype} on {q.device}")
-    if Hkv <= 0 or Hq % Hkv != 0:
-        raise ValueError(f"{Hq} query heads are not a multiple of {Hkv} kv heads")
-    Bt, mp = _table(table, lens, q.device)
-    if Bt != B:
-        raise ValueError(f"table: {Bt} sequences, q has {B}")
-    _expect("gain", gain, (Hq,), torch.float32, q.device)
-    _expect("temp", temp, (Hq,), torch.float32, q.device)
-    _expect("out", out, (B, Hq, dh), q.dtype, q.device)
-    _expect("lse", lse, (Hq, B), torch.float32, q.device)
+    workspace: "auto" (allocate one), None (no split), or paged_attention_workspace(...), which a
+    decoding loop keeps.  Returns (out [B, Hq, d], lse [Hq, B] or None)."""
+    dt, i, f32 = q.dtype, q.get_device(), torch.float32
+    shape, pool = q.shape, k_pages.shape
     if workspace is not None and not isinstance(workspace, str):
         _workspace(workspace, q.device)
-    _need_cuda(q, k_pages, v_pages, table, lens)
-    with _on(q.device):
+    if not (i >= 0 and len(shape) == 3 and len(pool) == 4 and pool[3] == shape[2]
+            and q.is_contiguous() and pool[1] > 0 and shape[1] % pool[1] == 0
+            and _fits(k_pages, pool, dt, i) and _fits(v_pages, pool, dt, i)
+            and _fits(table, (shape[0], table.shape[-1]), torch.int32, i)
+            and _fits(lens, shape[:1], torch.int32, i)
+            and (logsig_pages is None or _fits(logsig_pages, pool[::2], f32, i))
+            and (gain is None or _fits(gain, shape[1:2], f32, i))
+            and (temp is None or _fits(temp, shape[1:2], f32, i))
+            and (out is None or _fits(out, shape, dt, i))
+            and (lse is None or _fits(lse, shape[1::-1], f32, i))):
+        _expect_paged_attention(q, k_pages, v_pages, table, lens, logsig_pages, gain, temp, out,
+                                lse)
+    B, Hq, dh = shape
+    P, Hkv, page, _ = pool
+    with _on(i):
         one = torch.ones(Hq, device=q.device) if gain is None or temp is None else None
         gain = one if gain is None else gain
         temp = one if temp is None else temp
         out = torch.empty_like(q) if out is None else out
         if want_lse and lse is None:
-            lse = torch.empty((Hq, B), dtype=torch.float32, device=q.device)
+            lse = torch.empty((Hq, B), dtype=f32, device=q.device)
         if isinstance(workspace, str):
-            workspace = paged_attention_workspace(B, Hq, Hkv, dh, q.dtype, q.device)
+            workspace = paged_attention_workspace(B, Hq, Hkv, dh, dt, q.device)
         # a workspace of no bytes has no address: the call needs none of it
-        ws = None if workspace is None or workspace.numel() == 0 else workspace
+        ws_bytes = 0 if workspace is None else workspace.numel()
         _check("tg_paged_attention", library().tg_paged_attention(
-            _ptr(q), _ptr(k_pages), _ptr(v_pages), _dtype_code(q), B, Hq, Hkv, dh, P, page,
-            _ptr(table), mp, _ptr(lens), _ptr(logsig_pages), _ptr(gain), _ptr(temp), _ptr(out),
-            _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel(), _stream(q.device)))
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _dtype_code(q), B, Hq, Hkv, dh,
+            P, page, table.data_ptr(), table.shape[1], lens.data_ptr(), _addr(logsig_pages),
+            gain.data_ptr(), temp.data_ptr(), out.data_ptr(), _addr(lse),
+            workspace.data_ptr() if ws_bytes else None, ws_bytes, _raw_stream(i)))
     return out, lse
+
+
+def _expect_cache_update(table, lens, refs, parent, cu_new, table_out, lens_out, refs_out, start,
+                         copy_src, copy_dst):
+    dev = table.device
+    _expect_table(table, lens, dev)
+    B, mp = table.shape
+    Bo = B if parent is None else parent.shape[0]
+    _expect("refs", refs, (refs.shape[0],), torch.int32, dev)
+    _expect("parent", parent, (Bo,), torch.int32, dev)
+    _expect("cu_new", cu_new, (Bo + 1,), torch.int32, dev)
+    _expect("table_out", table_out, (Bo, mp), torch.int32, dev)
+    _expect("refs_out", refs_out, refs.shape, torch.int32, dev)
+    for name, t in (("lens_out", lens_out), ("start", start), ("copy_src", copy_src),
+                    ("copy_dst", copy_dst)):
+        _expect(name, t, (Bo,), torch.int32, dev)
+    _need_cuda(table)
 
 
 def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_out=None,
@@ -812,33 +861,44 @@ def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_o
     Returns a CacheUpdate: table, lens, refs, start [B'] (position of the first new token, -1
     where the sequence did not grow), and copy_src, copy_dst [B'], the page copies for
     cache_copy_pages that have to run before anything is appended."""
-    dev = table.device
-    B, mp = _table(table, lens, dev)
-    P = refs.shape[0]
-    _expect("refs", refs, (P,), torch.int32, dev)
-    Bo = B if parent is None else parent.shape[0]
-    _expect("parent", parent, (Bo,), torch.int32, dev)
-    _expect("cu_new", cu_new, (Bo + 1,), torch.int32, dev)
-    _expect("table_out", table_out, (Bo, mp), torch.int32, dev)
-    _expect("refs_out", refs_out, (P,), torch.int32, dev)
-    for name, t in (("lens_out", lens_out), ("start", start), ("copy_src", copy_src),
-                    ("copy_dst", copy_dst)):
-        _expect(name, t, (Bo,), torch.int32, dev)
-    _need_cuda(table, lens, refs)
-    with _on(dev):
-        i32 = dict(dtype=torch.int32, device=dev)
-        table_out = torch.full((Bo, mp), -1, **i32) if table_out is None else table_out
-        small = (refs_out, lens_out, start, copy_src, copy_dst)
-        if any(t is None for t in small):
+    i, i32 = table.get_device(), torch.int32
+    shape, P = table.shape, refs.shape[0]
+    Bo = shape[0] if parent is None else parent.shape[0]
+    small = (lens_out, start, copy_src, copy_dst)
+    if not (i >= 0 and len(shape) == 2 and _fits(table, shape, i32, i)
+            and _fits(lens, shape[:1], i32, i) and _fits(refs, (P,), i32, i)
+            and (parent is None or _fits(parent, (Bo,), i32, i))
+            and (cu_new is None or _fits(cu_new, (Bo + 1,), i32, i))
+            and (table_out is None or _fits(table_out, (Bo, shape[1]), i32, i))
+            and (refs_out is None or _fits(refs_out, (P,), i32, i))
+            and all(t is None or _fits(t, (Bo,), i32, i) for t in small)):
+        _expect_cache_update(table, lens, refs, parent, cu_new, table_out, lens_out, refs_out,
+                             start, copy_src, copy_dst)
+    B, mp = shape
+    with _on(i):
+        if table_out is None:
+            table_out = torch.full((Bo, mp), -1, dtype=i32, device=table.device)
+        refs_out = torch.empty_like(refs) if refs_out is None else refs_out
+        if lens_out is None or start is None or copy_src is None or copy_dst is None:
             # one allocation for those that are not given
-            fresh = torch.empty(P + 4 * Bo, **i32).split((P, Bo, Bo, Bo, Bo))
-            small = [f if t is None else t for f, t in zip(fresh, small)]
-        refs_out, lens_out, start, copy_src, copy_dst = small
+            fresh = torch.empty((4, Bo), dtype=i32, device=table.device).unbind()
+            lens_out, start, copy_src, copy_dst = [f if t is None else t
+                                                   for f, t in zip(fresh, small)]
         _check("tg_cache_update", library().tg_cache_update(
-            _ptr(table), _ptr(lens), B, _ptr(refs), P, page_size, mp, _ptr(parent), Bo,
-            _ptr(cu_new), _ptr(table_out), _ptr(lens_out), _ptr(refs_out), _ptr(start),
-            _ptr(copy_src), _ptr(copy_dst), _stream(dev)))
+            table.data_ptr(), lens.data_ptr(), B, refs.data_ptr(), P, page_size, mp,
+            _addr(parent), Bo, _addr(cu_new), table_out.data_ptr(), lens_out.data_ptr(),
+            refs_out.data_ptr(), start.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(),
+            _raw_stream(i)))
     return CacheUpdate(table_out, lens_out, refs_out, start, copy_src, copy_dst)
+
+
+def _expect_cache_compact(table, lens, refs, table_out, refs_out):
+    dev = table.device
+    _expect_table(table, lens, dev)
+    _expect("refs", refs, (refs.shape[0],), torch.int32, dev)
+    _expect("table_out", table_out, table.shape, torch.int32, dev)
+    _expect("refs_out", refs_out, refs.shape, torch.int32, dev)
+    _need_cuda(table)
 
 
 def cache_compact(table, lens, refs, page_size, table_out=None, refs_out=None):
@@ -848,22 +908,23 @@ def cache_compact(table, lens, refs, page_size, table_out=None, refs_out=None):
     refs), page_map [P] (a live page's new number, -1 for free ones), copy_src and copy_dst [P]
     (the moves, -1 behind them) and counts [2] = live pages, moves.  The moves are made by
     cache_copy_pages(pools, copy_src, copy_dst, counts[1:])."""
-    dev = table.device
-    B, mp = _table(table, lens, dev)
-    P = refs.shape[0]
-    _expect("refs", refs, (P,), torch.int32, dev)
-    _expect("table_out", table_out, (B, mp), torch.int32, dev)
-    _expect("refs_out", refs_out, (P,), torch.int32, dev)
-    _need_cuda(table, lens, refs)
-    with _on(dev):
-        i32 = dict(dtype=torch.int32, device=dev)
-        table_out = torch.full((B, mp), -1, **i32) if table_out is None else table_out
-        fresh = torch.empty(4 * P + 2, **i32).split((P, P, P, P, 2))
-        page_map, src, dst, counts = fresh[1:]
-        refs_out = fresh[0] if refs_out is None else refs_out
+    i, i32 = table.get_device(), torch.int32
+    shape, P = table.shape, refs.shape[0]
+    if not (i >= 0 and len(shape) == 2 and _fits(table, shape, i32, i)
+            and _fits(lens, shape[:1], i32, i) and _fits(refs, (P,), i32, i)
+            and (table_out is None or _fits(table_out, shape, i32, i))
+            and (refs_out is None or _fits(refs_out, (P,), i32, i))):
+        _expect_cache_compact(table, lens, refs, table_out, refs_out)
+    with _on(i):
+        if table_out is None:
+            table_out = torch.full(shape, -1, dtype=i32, device=table.device)
+        refs_out = torch.empty_like(refs) if refs_out is None else refs_out
+        page_map, src, dst = torch.empty((3, P), dtype=i32, device=table.device).unbind()
+        counts = torch.empty(2, dtype=i32, device=table.device)
         _check("tg_cache_compact", library().tg_cache_compact(
-            _ptr(table), _ptr(lens), B, _ptr(refs), P, page_size, mp, _ptr(table_out),
-            _ptr(refs_out), _ptr(page_map), _ptr(src), _ptr(dst), _ptr(counts), _stream(dev)))
+            table.data_ptr(), lens.data_ptr(), shape[0], refs.data_ptr(), P, page_size, shape[1],
+            table_out.data_ptr(), refs_out.data_ptr(), page_map.data_ptr(), src.data_ptr(),
+            dst.data_ptr(), counts.data_ptr(), _raw_stream(i)))
     return CacheCompact(table_out, refs_out, page_map, src, dst, counts)
 
 
@@ -873,26 +934,44 @@ def cache_copy_pages(pools, copy_src, copy_dst, count=None):
     (None: all).  No page may be a destination twice, nor both a source and a destination."""
     if len(pools) > MAX_GATHER_TENSORS:
         raise ValueError("too many pools")
-    n = copy_src.shape[0]
-    dev = copy_src.device
-    _expect("copy_src", copy_src, (n,), torch.int32, dev)
-    _expect("copy_dst", copy_dst, (n,), torch.int32, dev)
-    _expect("count", count, (1,), torch.int32, dev)
+    n, i, i32 = copy_src.shape[0], copy_src.get_device(), torch.int32
+    if not (i >= 0 and _fits(copy_src, (n,), i32, i) and _fits(copy_dst, (n,), i32, i)
+            and (count is None or _fits(count, (1,), i32, i))):
+        _expect("copy_src", copy_src, (n,), i32, copy_src.device)
+        _expect("copy_dst", copy_dst, (n,), i32, copy_src.device)
+        _expect("count", count, (1,), i32, copy_src.device)
+    P = None
+    arr = (PagePool * max(len(pools), 1))()
+    for t, a in zip(pools, arr):
+        shape = t.shape
+        P = shape[1] if P is None and len(shape) > 1 else P
+        if len(shape) < 3 or shape[1] != P or t.get_device() != i or not t.is_contiguous():
+            raise ValueError(f"pools: {tuple(shape)} on {t.device}, expected contiguous "
+                             f"[layers, {P}, ...] on {copy_src.device}")
+        a.base = t.data_ptr()
+        a.page_bytes = math.prod(shape[2:]) * t.element_size()
+        a.layers = shape[0]
+    _need_cuda(copy_src)
     if not pools:
         return
-    P = pools[0].shape[1] if pools[0].dim() > 1 else -1
-    arr = (PagePool * len(pools))()
-    for i, t in enumerate(pools):
-        if t.dim() < 3 or t.shape[1] != P:
-            raise ValueError(f"pools[{i}]: shape {tuple(t.shape)}, expected [layers, {P}, ...]")
-        _expect(f"pools[{i}]", t, t.shape, t.dtype, dev)
-        arr[i].base = t.data_ptr()
-        arr[i].page_bytes = math.prod(t.shape[2:]) * t.element_size()
-        arr[i].layers = t.shape[0]
-    _need_cuda(copy_src, *pools)
-    with _on(dev):
+    with _on(i):
         _check("tg_cache_copy_pages", library().tg_cache_copy_pages(
-            arr, len(pools), P, _ptr(copy_src), _ptr(copy_dst), n, _ptr(count), _stream(dev)))
+            arr, len(pools), P, copy_src.data_ptr(), copy_dst.data_ptr(), n, _addr(count),
+            _raw_stream(i)))
+
+
+def _expect_cache_append(k, v, cu_new, start, table, k_pages, v_pages, logsig, logsig_pages):
+    _expect_pools(k_pages, v_pages, logsig_pages)
+    dev, rows = k_pages.device, k.shape[0]
+    _, Hkv, _, d = k_pages.shape
+    _expect("k", k, (rows, Hkv, d), k_pages.dtype, dev)
+    _expect("v", v, (rows, Hkv, d), k_pages.dtype, dev)
+    _expect("logsig", logsig, (rows,), torch.float32, dev)
+    _expect_table(table, None, dev)
+    B = table.shape[0]
+    _expect("cu_new", cu_new, (B + 1,), torch.int32, dev)
+    _expect("start", start, (B,), torch.int32, dev)
+    _need_cuda(k)
 
 
 def cache_append(k, v, cu_new, start, table, k_pages, v_pages, logsig=None, logsig_pages=None):
@@ -900,23 +979,40 @@ def cache_append(k, v, cu_new, start, table, k_pages, v_pages, logsig=None, logs
     pages: row i of sequence b (cu_new[b] <= i < cu_new[b + 1]) becomes token
     start[b] + i - cu_new[b]; start[b] < 0 skips the sequence.  cu_new [B + 1], start [B],
     table [B, max_pages]: int32 on the device."""
-    P, Hkv, page, d = _pools(k_pages, v_pages, logsig_pages)
-    dev = k_pages.device
-    rows = k.shape[0]
-    _expect("k", k, (rows, Hkv, d), k_pages.dtype, dev)
-    _expect("v", v, (rows, Hkv, d), k_pages.dtype, dev)
-    _expect("logsig", logsig, (rows,), torch.float32, dev)
     if logsig is not None and logsig_pages is None:
         raise ValueError("logsig without logsig_pages")
-    B, mp = _table(table, None, dev)
-    _expect("cu_new", cu_new, (B + 1,), torch.int32, dev)
-    _expect("start", start, (B,), torch.int32, dev)
-    _need_cuda(k, v, cu_new, start, table, k_pages)
-    with _on(dev):
+    i, i32, f32, dt = k.get_device(), torch.int32, torch.float32, k.dtype
+    rows, pool, shape = k.shape[0], k_pages.shape, table.shape
+    if not (i >= 0 and len(pool) == 4 and len(shape) == 2 and _fits(k_pages, pool, dt, i)
+            and _fits(v_pages, pool, dt, i) and _fits(k, (rows, pool[1], pool[3]), dt, i)
+            and _fits(v, k.shape, dt, i) and _fits(table, shape, i32, i)
+            and _fits(cu_new, (shape[0] + 1,), i32, i) and _fits(start, shape[:1], i32, i)
+            and (logsig is None or _fits(logsig, (rows,), f32, i))
+            and (logsig_pages is None or _fits(logsig_pages, pool[::2], f32, i))):
+        _expect_cache_append(k, v, cu_new, start, table, k_pages, v_pages, logsig, logsig_pages)
+    with _on(i):
         _check("tg_cache_append", library().tg_cache_append(
-            _ptr(k), _ptr(v), _ptr(logsig), _dtype_code(k), rows, B, _ptr(cu_new), _ptr(start),
-            Hkv, d, P, page, _ptr(table), mp, _ptr(k_pages), _ptr(v_pages), _ptr(logsig_pages),
-            _stream(dev)))
+            k.data_ptr(), v.data_ptr(), _addr(logsig), _dtype_code(k), rows, shape[0],
+            cu_new.data_ptr(), start.data_ptr(), pool[1], pool[3], pool[0], pool[2],
+            table.data_ptr(), shape[1], k_pages.data_ptr(), v_pages.data_ptr(),
+            _addr(logsig_pages), _raw_stream(i)))
+
+
+def _expect_delta_step(q, k, v, log_alpha, beta, state, parent, out, state_out):
+    if q.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be [batch, heads, head_dim], state [n, heads, head_dim, head_dim]")
+    B, H, d = q.shape
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        _expect(name, t, (B, H, d), q.dtype, dev)
+    _expect("log_alpha", log_alpha, (B, H), torch.float32, dev)
+    _expect("beta", beta, (B, H), torch.float32, dev)
+    _expect("state", state, (state.shape[0], H, d, d), torch.float32, dev)
+    _expect("parent", parent, (B,), torch.int32, dev)
+    _expect("state_out", state_out, (B, H, d, d), torch.float32, dev)
+    if parent is None and state.shape[0] < B:
+        raise ValueError(f"state: {state.shape[0]} states for {B} sequences")
+    _need_cuda(q)
 
 
 def gated_delta_step(q, k, v, log_alpha, beta, state, parent=None, eps=1e-6, out=None,
@@ -928,29 +1024,25 @@ def gated_delta_step(q, k, v, log_alpha, beta, state, parent=None, eps=1e-6, out
     reordering of a beam search; state_out may then not be state.  Without parents sequence b
     starts from state[b], and state_out=state updates in place.
     Returns (out [B, H, d], state_out [B, H, d, d])."""
-    if q.dim() != 3 or state.dim() != 4:
-        raise ValueError("q must be [batch, heads, head_dim], state [n, heads, head_dim, head_dim]")
-    B, H, d = q.shape
-    dev = q.device
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _expect(name, t, (B, H, d), q.dtype, dev)
-    _expect("log_alpha", log_alpha, (B, H), torch.float32, dev)
-    _expect("beta", beta, (B, H), torch.float32, dev)
-    S = state.shape[0]
-    _expect("state", state, (S, H, d, d), torch.float32, dev)
-    _expect("parent", parent, (B,), torch.int32, dev)
-    _expect("out", out, (B, H, d), q.dtype, dev)
-    _expect("state_out", state_out, (B, H, d, d), torch.float32, dev)
-    if parent is None and S < B:
-        raise ValueError(f"state: {S} states for {B} sequences")
-    _need_cuda(q, k, v, state)
-    with _on(dev):
+    i, f32, dt = q.get_device(), torch.float32, q.dtype
+    shape, S = q.shape, state.shape[0]
+    full = shape + shape[-1:]  # [B, H, d, d]
+    if not (i >= 0 and len(shape) == 3 and q.is_contiguous() and _fits(k, shape, dt, i)
+            and _fits(v, shape, dt, i) and _fits(log_alpha, shape[:2], f32, i)
+            and _fits(beta, shape[:2], f32, i) and _fits(state, (S,) + full[1:], f32, i)
+            and (parent is None or _fits(parent, shape[:1], torch.int32, i))
+            and (out is None or _fits(out, shape, dt, i))
+            and (state_out is None or _fits(state_out, full, f32, i))
+            and (parent is not None or S >= shape[0])):
+        _expect_delta_step(q, k, v, log_alpha, beta, state, parent, out, state_out)
+    with _on(i):
         out = torch.empty_like(q) if out is None else out
         if state_out is None:
-            state_out = torch.empty((B, H, d, d), dtype=torch.float32, device=dev)
+            state_out = torch.empty(full, dtype=f32, device=q.device)
         _check("tg_gated_delta_step", library().tg_gated_delta_step(
-            _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(log_alpha), _ptr(beta), B, H, d,
-            float(eps), _ptr(state), S, _ptr(parent), _ptr(state_out), _ptr(out), _stream(dev)))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), log_alpha.data_ptr(),
+            beta.data_ptr(), shape[0], shape[1], shape[2], eps, state.data_ptr(), S,
+            _addr(parent), state_out.data_ptr(), out.data_ptr(), _raw_stream(i)))
     return out, state_out
 
 
@@ -973,19 +1065,22 @@ def beam_select(logits, scores, n_out=None, workspace=None):
         raise ValueError("logits must be [groups * beams, vocab], scores [groups, beams]")
     G, beams = scores.shape
     V = logits.shape[1]
-    dev = logits.device
-    _expect("logits", logits, (G * beams, V), logits.dtype, dev)
-    _expect("scores", scores, (G, beams), torch.float32, dev)
-    n_out = beams if n_out is None else int(n_out)
+    i, dev = logits.get_device(), logits.device
     if workspace is not None:
         _workspace(workspace, dev)
-    _need_cuda(logits, scores)
-    with _on(dev):
+    if not (i >= 0 and _fits(logits, (G * beams, V), logits.dtype, i)
+            and _fits(scores, (G, beams), torch.float32, i)):
+        _expect("logits", logits, (G * beams, V), logits.dtype, dev)
+        _expect("scores", scores, (G, beams), torch.float32, dev)
+        _need_cuda(logits)
+    n_out = beams if n_out is None else n_out
+    with _on(i):
         if workspace is None:
             workspace = beam_select_workspace(G, beams, V, n_out, dev)
-        best = torch.empty((G, n_out), dtype=torch.float32, device=dev)
-        parent, token = torch.empty((2, G, n_out), dtype=torch.int32, device=dev).unbind()
+        best, parent, token = torch.empty((3, G, n_out), dtype=torch.int32, device=dev).unbind()
+        best = best.view(torch.float32)
         _check("tg_beam_select", library().tg_beam_select(
-            _ptr(logits), _dtype_code(logits), _ptr(scores), G, beams, V, n_out, _ptr(best),
-            _ptr(parent), _ptr(token), _ptr(workspace), workspace.numel(), _stream(dev)))
+            logits.data_ptr(), _dtype_code(logits), scores.data_ptr(), G, beams, V, n_out,
+            best.data_ptr(), parent.data_ptr(), token.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _raw_stream(i)))
     return best, parent, token

@@ -31,7 +31,7 @@ tg_status check_heads(tg_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int
   if (dtype != TG_BF16 && dtype != TG_FP32) return set_error(TG_ERR_DTYPE, "dtype %d", dtype);
   if (n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0)
     return set_error(TG_ERR_SHAPE, "n_q_heads=%d n_kv_heads=%d", n_q_heads, n_kv_heads);
-  if (n_q_heads > 1024) return set_error(TG_ERR_UNSUPPORTED, "n_q_heads=%d exceeds 1024", n_q_heads);
+  if (n_q_heads > 512) return set_error(TG_ERR_UNSUPPORTED, "n_q_heads=%d exceeds 512", n_q_heads);
   if (head_dim != 64 && head_dim != 128)
     return set_error(TG_ERR_UNSUPPORTED, "head_dim=%d (supported: 64, 128)", head_dim);
   return TG_OK;

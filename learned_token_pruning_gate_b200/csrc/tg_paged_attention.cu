@@ -45,6 +45,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxHeads = 512;  // query heads, as the C ABI checks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // how far a logit may exceed the reference maximum
 
@@ -58,6 +59,11 @@ __host__ __device__ constexpr int ctas_per_sm(bool bf16, int heads, int head_dim
   return bf16 ? (heads == 8 ? 3 : 2) : (heads == 1 || (heads == 2 && head_dim == 64) ? 3 : 2);
 }
 
+// A partial sum: [heads][d], then the heads' maxima and their sums; a multiple of 16 bytes.
+__host__ __device__ constexpr int slot_floats(int heads, int head_dim) {
+  return heads * head_dim + (2 * heads + 3) / 4 * 4;
+}
+
 struct Plan {
   PagedAttnArgs a;
   int32_t group;       // query heads per kv head
@@ -65,7 +71,7 @@ struct Plan {
   int32_t units;       // units per sequence: hkv * blocks
   int2* shares;        // [batch * units] the first and last CTA of a shared unit, {0, -1} otherwise; or null:
                        // every unit is whole
-  float* partial;      // [2 * grid][heads][d + 2]
+  float* partial;      // [2 * grid] slots
 };
 
 // 16 bytes of a row, not kept in L1 (each is used once).
@@ -148,14 +154,15 @@ struct CoreBf16 {
       for (int c = 0; c < kKv; ++c)
         q[n][c] = 8 * n + g() < nh ? load_row16(qp + (8 * n + g()) * D + t() * 8 + c * 32) : make_uint4(0u, 0u, 0u, 0u);
   }
-  __device__ __forceinline__ void begin(const Plan& p, int h0, int nh) {
+  __device__ __forceinline__ void begin(const float2* heads, int nh) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int h = 8 * n + 2 * t() + e;
-        scale[n][e] = h < nh ? 1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h0 + h]) : 0.0f;
-        gain[n][e] = h < nh ? p.a.gain[h0 + h] : 0.0f;
+        const float2 x = h < nh ? heads[h] : make_float2(0.0f, 0.0f);
+        scale[n][e] = x.x;
+        gain[n][e] = x.y;
         m[n][e] = -INFINITY;
         l[n][e] = 0.0f;
       }
@@ -335,11 +342,12 @@ struct CoreFp32 {
 #pragma unroll
       for (int c = 0; c < kVec; ++c) q[h][c] = h < nh ? load4(qp + h * D + c * 32) : zero();
   }
-  __device__ __forceinline__ void begin(const Plan& p, int h0, int nh) {
+  __device__ __forceinline__ void begin(const float2* heads, int nh) {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      scale[h] = h < nh ? 1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h0 + h]) : 0.0f;
-      gain[h] = h < nh ? p.a.gain[h0 + h] : 0.0f;
+      const float2 x = h < nh ? heads[h] : make_float2(0.0f, 0.0f);
+      scale[h] = x.x;
+      gain[h] = x.y;
       m[h] = -INFINITY;
       l[h] = 0.0f;
 #pragma unroll
@@ -453,6 +461,14 @@ struct CoreFp32 {
 
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  uint2 u;
+  memcpy(&u.x, &a, 4);
+  memcpy(&u.y, &b, 4);
+  *reinterpret_cast<uint2*>(p) = u;
+}
 
 // A place in the list of tiles: tile j of unit u of sequence b.
 struct Place {
@@ -465,9 +481,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
   constexpr int H = Core::kHeads;
   constexpr int kGroups = Core::kKeys / 16;      // groups of 16 keys of a warp
   constexpr int kTile = Core::kKeys * kWarps;
-  constexpr int kSlot = H * (D + 2);  // floats of a partial sum: [H][D], then the maxima and the sums
+  constexpr int kSlot = slot_floats(H, D);
   __shared__ int ends[kMaxSeqs];      // inclusive scan of the sequences' tiles (per unit)
   __shared__ int lens[kMaxSeqs];
+  __shared__ float2 heads[kMaxHeads];  // 1 / (sqrt(d) temp) and the gain
   __shared__ int warp_sums[kWarps];
   __shared__ float part_m[kWarps * H], part_l[kWarps * H];
   __shared__ __align__(16) float part_o[kWarps * H * D];
@@ -480,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
   const int batch = p.a.batch;
   const int run = (batch + kThreads - 1) / kThreads;
   const int64_t most = static_cast<int64_t>(p.a.max_pages) << p.a.page_shift;
+  for (int h = tid; h < p.a.hq; h += kThreads)
+    heads[h] = make_float2(1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h]), p.a.gain[h]);
   int sum = 0;
   for (int i = 0; i < run; ++i) {
     const int b = tid * run + i;
@@ -534,26 +553,30 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
   // The join of kWarps sums in shared memory, into the output or into a slot for the second kernel.
   auto finish = [&](int b, int h0, int nh, float* slot) {
     __syncthreads();
-    for (int i = tid; i < nh * D; i += kThreads) {
+    for (int i = tid * 4; i < nh * D; i += kThreads * 4) {
       const int h = i / D, d = i - h * D;
-      float top = -INFINITY, l = 0.0f, x = 0.0f;
+      float top = -INFINITY, l = 0.0f;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w * H + h]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float c = weight(part_m[w * H + h], top);
+        const float4 o = *reinterpret_cast<const float4*>(part_o + (w * H + h) * D + d);
         l = fmaf(part_l[w * H + h], c, l);
-        x = fmaf(part_o[(w * H + h) * D + d], c, x);
+        x = make_float4(fmaf(o.x, c, x.x), fmaf(o.y, c, x.y), fmaf(o.z, c, x.z), fmaf(o.w, c, x.w));
       }
       if (slot) {
-        slot[i] = x;
+        *reinterpret_cast<float4*>(slot + i) = x;
         if (d == 0) {
           slot[H * D + h] = top;
           slot[H * D + H + h] = l;
         }
       } else {
         // nothing left of the sequence: 0 and -inf (a sum of nothing is 0, any other holds its reference's weight 1)
-        put(static_cast<T*>(p.a.out) + (static_cast<int64_t>(b) * p.a.hq + h0 + h) * D + d, l == 0.0f ? 0.0f : x / l);
+        const float c = l == 0.0f ? 0.0f : 1.0f / l;
+        put4(static_cast<T*>(p.a.out) + (static_cast<int64_t>(b) * p.a.hq + h0 + h) * D + d,
+             make_float4(x.x * c, x.y * c, x.z * c, x.w * c));
         if (d == 0 && p.a.lse) p.a.lse[static_cast<int64_t>(h0 + h) * batch + b] = l == 0.0f ? -INFINITY : top + logf(l);
       }
     }
@@ -589,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
     core.load_k(p, keys, 0);
     core.load_v(p, keys, 0);
     core.load_q(p, now.b, h0, nh);
-    core.begin(p, h0, nh);
+    core.begin(heads + h0, nh);
     int j0 = now.j;  // where the present unit was entered
     for (;; ++at) {
       // the next tile, whose rows are requested before this one's are used up
@@ -633,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
               whole ? make_int2(0, -1) : make_int2(blockIdx.x, static_cast<int>(last / per));
         }
         if (!more) break;
-        core.begin(p, next_h0, next_nh);
+        core.begin(heads + next_h0, next_nh);
         j0 = 0;
       }
       now = next;
@@ -675,7 +698,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const int b = static_cast<int>(unit / p.units), u = static_cast<int>(unit - static_cast<int64_t>(b) * p.units);
   const int hk = u / p.blocks, block = u - hk * p.blocks, h = blockIdx.y;
   if (h >= p.group - block * heads) return;
-  const int64_t slot = static_cast<int64_t>(heads) * (D + 2);
+  const int64_t slot = slot_floats(heads, D);
   float m = -INFINITY, l = 0.0f, o[kPer] = {};
   for (int c = share.x + warp; c <= share.y; c += 4 * kJoinWarps) {
     float pm[4], pl[4], po[4][kPer];
@@ -758,7 +781,7 @@ Shape shape_of(bool bf16, int batch, int hq, int hkv, int head_dim) {
   s.units = hkv * s.blocks;
   s.grid = num_sms() * ctas_per_sm(bf16, s.heads, head_dim);
   s.share_bytes = (static_cast<size_t>(batch) * s.units * sizeof(int2) + 255) / 256 * 256;
-  s.slot_bytes = sizeof(float) * s.heads * (head_dim + 2);
+  s.slot_bytes = sizeof(float) * slot_floats(s.heads, head_dim);
   return s;
 }
 

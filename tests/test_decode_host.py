@@ -292,8 +292,8 @@ def test_binding_rejects_mismatched_operands():
     _raises("too many", tg.cache_copy_pages, [pool] * 9, i32(1), i32(1))
     _raises("copy_dst", tg.cache_copy_pages, [pool], i32(2), i32(1))
     _raises("count", tg.cache_copy_pages, [pool], i32(1), i32(1), i32(2))
-    _raises(r"pools\[1\]", tg.cache_copy_pages, [pool, torch.zeros(2, 6, 16)], i32(1), i32(1))
-    _raises(r"pools\[0\]", tg.cache_copy_pages, [torch.zeros(5)], i32(1), i32(1))
+    _raises("pools: ", tg.cache_copy_pages, [pool, torch.zeros(2, 6, 16)], i32(1), i32(1))
+    _raises("pools: ", tg.cache_copy_pages, [torch.zeros(5)], i32(1), i32(1))
     k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     args = lambda **kw: [kw.get(n, x) for n, x in dict(k=k, v=k, cu=i32(3), st=i32(2), t=t, kp=a[1], vp=a[2]).items()]  # noqa: E731
     for match, kw in (("k: dtype", dict(k=k.float())), ("v: shape", dict(v=k[:2])), ("cu_new", dict(cu=i32(2))),
