@@ -7,6 +7,10 @@ library calls on one stream with no allocation and no host synchronisation --
 the form that CUDA-graph capture and per-kernel timing need.  The gate counts
 the selection's first radix pass into the layer's top-K workspace
 (tg_gate_score_hist), and the selection starts from it (tg_topk_select_ws).
+
+``GatedStack`` runs the upper layers over the kept rows, ``PagedCache`` keeps what
+they emit in pages that sequences share, and ``GatedDecoder`` decodes from it one
+token at a time, for single sequences and for the beams of a search.
 """
 from __future__ import annotations
 
@@ -16,8 +20,9 @@ import numpy as np
 import torch
 
 from . import (ALGO_AUTO, GatherTensor, _check, _dtype_code, _host_i32,
-               attention_workspace_bytes, gated_attention, kept_offsets, library, qkv_rope_emit,
-               rmsnorm, swiglu, topk_workspace_bytes)
+               attention_workspace_bytes, cache_append, cache_compact, cache_copy_pages,
+               cache_update, gated_attention, kept_offsets, library, paged_attention,
+               paged_attention_workspace, qkv_rope_emit, rmsnorm, swiglu, topk_workspace_bytes)
 
 
 class GatedLayer:
@@ -200,3 +205,148 @@ class GatedStack:
             b = rmsnorm(x, ly["w_ln2"], self.eps)
             x.addmm_(swiglu(torch.mm(b, self.wgu[i].t())), ly["wd"].t())
         return x, self.cache_k, self.cache_v
+
+
+class PagedCache:
+    """The k, v and log-gates of a batch's sequences, in pages that they share.
+
+    k, v: [layers, pages, Hkv, page_size, d]; logsig: [pages, page_size] fp32, one for all
+    layers.  grow() makes room for new tokens (and forks or frees sequences), append() writes a
+    layer's rows there, attend() reads them; nothing of it waits for the GPU or allocates.  A
+    captured graph may hold any of these calls; the tables of a fork alternate between two
+    buffers, so capture forks in pairs.
+
+    After grow(), start [batch] holds the position of each sequence's first new token, -1 where it
+    did not fit (its rows are then skipped by append())."""
+
+    def __init__(self, layers, pages, n_kv_heads, page_size, head_dim, batch, max_pages,
+                 dtype=torch.bfloat16, device="cuda", with_gates=True):
+        shape = (layers, pages, n_kv_heads, page_size, head_dim)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.page_size, self.batch = page_size, batch
+        self.k = torch.zeros(shape, dtype=dtype, device=device)
+        self.v = torch.zeros(shape, dtype=dtype, device=device)
+        self.logsig = torch.zeros((pages, page_size), device=device) if with_gates else None
+        self._tables = [torch.full((batch, max_pages), -1, **i32) for _ in range(2)]
+        self._lens = [torch.zeros(batch, **i32) for _ in range(2)]
+        self._now = 0
+        self.refs = torch.zeros(pages, **i32)
+        self.start, self._src, self._dst = (torch.empty(batch, **i32) for _ in range(3))
+        self.cu_new = torch.arange(batch + 1, **i32)
+        self._one_each = self.cu_new
+        self._ws = {}
+
+    @property
+    def table(self):
+        return self._tables[self._now]
+
+    @property
+    def lens(self):
+        return self._lens[self._now]
+
+    @property
+    def _pools(self):
+        pools = [self.k, self.v]
+        return pools if self.logsig is None else pools + [self.logsig.unsqueeze(0)]
+
+    def grow(self, cu_new=None, parent=None):
+        """Room for cu_new[b + 1] - cu_new[b] tokens (None: one) in every sequence b, after
+        sequence b has become a fork of sequence parent[b] (-1: empty; None: itself).  Both int32
+        on the device; pages that no sequence holds any more are free again."""
+        self.cu_new = self._one_each if cu_new is None else cu_new
+        to = self._now if parent is None else 1 - self._now
+        cache_update(self.table, self.lens, self.refs, self.page_size, parent, self.cu_new,
+                     self._tables[to], self._lens[to], self.refs, self.start, self._src, self._dst)
+        self._now = to
+        cache_copy_pages(self._pools, self._src, self._dst)
+
+    def free(self, keep):
+        """Frees every sequence b with keep[b] < 0 (keep: int32 on the device, b itself or -1)."""
+        to = 1 - self._now
+        cache_update(self.table, self.lens, self.refs, self.page_size, keep, None,
+                     self._tables[to], self._lens[to], self.refs, self.start, self._src, self._dst)
+        self._now = to
+
+    def append(self, layer, k, v, logsig=None):
+        """Writes one layer's new rows k, v [rows, Hkv, d], packed as the last grow() was told, and
+        (once per token, with layer 0) their log-gates; None: 0."""
+        gates = self.logsig if layer == 0 else None
+        cache_append(k, v, self.cu_new, self.start, self.table, self.k[layer], self.v[layer],
+                     logsig if gates is not None else None, gates)
+
+    def attend(self, layer, q, gain=None, temp=None, out=None, lse=None):
+        """Gated attention of one query q [batch, Hq, d] per sequence over its cached tokens."""
+        if q.shape[1] not in self._ws:
+            self._ws[q.shape[1]] = paged_attention_workspace(
+                self.batch, q.shape[1], self.k.shape[2], self.k.shape[4], q.dtype, q.device)
+        return paged_attention(q, self.k[layer], self.v[layer], self.table, self.lens, self.logsig,
+                               gain, temp, out=out, lse=lse, workspace=self._ws[q.shape[1]])[0]
+
+    def compact(self):
+        """Moves the pages in use to the front of the pool.  Returns counts [2] on the device: how
+        many pages are in use, how many were moved."""
+        c = cache_compact(self.table, self.lens, self.refs, self.page_size, table_out=self.table,
+                          refs_out=self.refs)
+        cache_copy_pages(self._pools, c.copy_src, c.copy_dst, c.counts[1:])
+        return c.counts
+
+
+class GatedDecoder:
+    """Decodes through a GatedStack's layers from the cache its prefill emits.
+
+    prefill(x) runs the stack over the kept rows and puts the emitted cache into pages;
+    step(x, parent) runs one new token per sequence: x [batch, d_model], the residuals at the
+    gated layers' input.  New tokens take the positions behind their whole prompt (pruned tokens
+    included) and have no gate bias.  With `parent` [batch] int32 the sequences are first forked
+    from one another, as beam_select names the parents of a search's beams.
+
+    beams: sequences per prompt.  Sequence p * beams of prompt p gets the prefill; the first step
+    forks it (parent = p * beams for all of the prompt's beams)."""
+
+    def __init__(self, stack, pages, page_size, max_pages, beams=1):
+        self.stack, self.beams = stack, beams
+        self.n_prompts = len(stack.ck) - 1
+        self.batch = self.n_prompts * beams
+        dt, dev = stack.cache_k.dtype, stack.cache_k.device
+        self.cache = PagedCache(len(stack.layers), pages, stack.Hkv, page_size, stack.dh, self.batch,
+                                max_pages, dt, dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        lens = np.zeros((self.n_prompts, beams), np.int64)
+        lens[:, 0] = np.diff(stack.ck)
+        cu = np.concatenate([[0], np.cumsum(lens.reshape(-1))])
+        self.cu_prefill = torch.from_numpy(cu.astype(np.int32)).to(dev)
+        self.pos = torch.from_numpy(np.repeat(np.diff(stack.cu), beams).astype(np.int32)).to(dev)
+        self._every = np.array([0, np.iinfo(np.int32).max], np.int32)  # positions, as one prompt's rows
+        self._rows = np.array([0, self.batch], np.int32)
+        self.q = torch.empty((self.batch, stack.Hq, stack.dh), dtype=dt, device=dev)
+        self.k, self.v = (torch.empty((self.batch, stack.Hkv, stack.dh), dtype=dt, device=dev)
+                          for _ in range(2))
+        self.o = torch.empty_like(self.q)
+
+    def prefill(self, x):
+        """x [M, d_model] kept rows (overwritten with the stack's output, which is returned)."""
+        x, cache_k, cache_v = self.stack.run(x)
+        self.cache.grow(self.cu_prefill)
+        for i in range(len(self.stack.layers)):
+            self.cache.append(i, cache_k[i], cache_v[i], self.stack.logsig)
+        return x
+
+    def step(self, x, parent=None):
+        """x [batch, d_model] (overwritten with the output, which is returned)."""
+        st = self.stack
+        if parent is not None:
+            # (a freed sequence, parent -1, starts again at position 0)
+            self.pos.copy_(torch.where(parent >= 0, self.pos[parent.clamp(min=0).long()], 0))
+        self.cache.grow(parent=parent)
+        for i, ly in enumerate(st.layers):
+            a = rmsnorm(x, ly["w_ln1"], st.eps)
+            qkv = torch.mm(a, ly["wqkv"].t())
+            qkv_rope_emit(qkv, self._every, self._rows, self.pos, st.Hq, st.Hkv, st.dh, ly["w_qn"],
+                          ly["w_kn"], st.eps, st.theta, q_out=self.q, k_out=self.k, v_out=self.v)
+            self.cache.append(i, self.k, self.v)
+            self.cache.attend(i, self.q, ly["gain"], ly["temp"], out=self.o)
+            x.addmm_(self.o.view(self.batch, st.Hq * st.dh), ly["wo"].t())
+            b = rmsnorm(x, ly["w_ln2"], st.eps)
+            x.addmm_(swiglu(torch.mm(b, st.wgu[i].t())), ly["wd"].t())
+        self.pos += self.cache.start >= 0  # a sequence without room for its token did not move on
+        return x
