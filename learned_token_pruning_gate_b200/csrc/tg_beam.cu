@@ -217,11 +217,12 @@ __global__ void __launch_bounds__(kChunkThreads, 4)
   const int n = n_found;
   uint64_t* out = ws.keys + (row * chunks + chunk) * n_out;
   if (n <= kChunkKeys) {
-    for (int i = tid; i < n; i += kChunkThreads) {
+    for (int i = warp; i < n; i += kWarps) {  // a warp per key
       const uint64_t k = found[i];
       int above = 0;
-      for (int j = 0; j < n; ++j) above += found[j] > k;
-      if (above < n_out) out[above] = k;
+      for (int j = 0; j < n; j += 32)
+        above += __popc(__ballot_sync(0xffffffffu, j + lane < n && found[j + lane] > k));
+      if (lane == 0 && above < n_out) out[above] = k;
     }
     for (int i = n + tid; i < n_out; i += kChunkThreads) out[i] = 0;
   } else {
@@ -263,7 +264,8 @@ struct Cand {
   uint32_t place;
 };
 __device__ __forceinline__ bool before(const Cand& a, const Cand& b) {
-  return a.score > b.score || (a.score == b.score && a.place < b.place);
+  // (no short cut: the branches cost more than both comparisons)
+  return (a.score > b.score) | ((a.score == b.score) & (a.place < b.place));
 }
 __device__ __forceinline__ uint64_t order_key64(double x) {
   if (!(fabs(x) < INFINITY)) return 0;  // not finite: no candidate
@@ -301,6 +303,9 @@ __global__ void __launch_bounds__(kMergeThreads)
     n_found = 0;
   }
   if (tid < kMaxOut) ranked[tid] = -1;
+  // the heads' keys, on their way while the sums are joined
+  const uint64_t* const keys = ws.keys + row0 * chunks * n_out;
+  const uint64_t first_head = tid < lists ? keys[static_cast<int64_t>(tid) * n_out] : 0;
   // a warp per beam: log of the row's sum of exponentials
   for (int beam = warp; beam < beams; beam += kWarps) {
     const float2* part = ws.sums + (row0 + beam) * chunks;
@@ -319,9 +324,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     if (lane == 0) log_sum[beam] = static_cast<double>(top) * kInvLog2e + log(s);
   }
   __syncthreads();
-  auto cand = [&](int list, int i) {
+  auto cand = [&](int list, uint64_t key) {
     const int beam = list / chunks;
-    const uint64_t key = ws.keys[(row0 * chunks + list) * n_out + i];
     Cand c = {0, 0};
     if (key) {
       const uint32_t token = 0xFFFFFFFFu - static_cast<uint32_t>(key);
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     return c;
   };
   for (int l = tid; l < lists; l += kMergeThreads) {
-    const Cand c = cand(l, 0);
+    const Cand c = cand(l, l == tid ? first_head : keys[static_cast<int64_t>(l) * n_out]);
     head_score[l] = c.score;
     head_place[l] = c.place;
   }
@@ -341,8 +345,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     const Cand c = {head_score[l], head_place[l]};
     if (!c.score) continue;
     int above = 0;
-    for (int j = lane; j < lists; j += 32) above += before(Cand{head_score[j], head_place[j]}, c);
-    above = __reduce_add_sync(0xffffffffu, above);
+    for (int j = 0; j < lists; j += 32)
+      above += __popc(__ballot_sync(0xffffffffu, j + lane < lists && before(Cand{head_score[j + lane], head_place[j + lane]}, c)));
     if (lane == 0 && above < n_out) {
       ranked[above] = l;
       if (above == n_out - 1) limit = c;
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int l = ranked[r];
     if (l < 0) break;
     for (int i = lane; i < n_out - r; i += 32) {
-      const Cand c = cand(l, i);
+      const Cand c = cand(l, keys[static_cast<int64_t>(l) * n_out + i]);
       if (!c.score || before(limit, c)) continue;
       const int at = atomicAdd(&n_found, 1);
       found_score[at] = c.score;
@@ -368,8 +372,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int i = warp; i < n; i += kWarps) {
     const Cand c = {found_score[i], found_place[i]};
     int above = 0;
-    for (int j = lane; j < n; j += 32) above += before(Cand{found_score[j], found_place[j]}, c);
-    above = __reduce_add_sync(0xffffffffu, above);
+    for (int j = 0; j < n; j += 32)
+      above += __popc(__ballot_sync(0xffffffffu, j + lane < n && before(Cand{found_score[j + lane], found_place[j + lane]}, c)));
     if (lane != 0 || above >= n_out) continue;
     const uint32_t beam = c.place / static_cast<uint32_t>(vocab);
     scores_out[out + above] = static_cast<float>(from_order_key64(c.score));
