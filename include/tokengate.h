@@ -540,7 +540,8 @@ TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int3
  *   lens              [batch] int32 tokens per sequence
  *   refs              [n_pages] int32: how many table entries hold a page; 0 = free
  * All of it is device memory that the host never has to read, so a step can be
- * captured in a CUDA graph.  The host cannot check what lies there; a kernel
+ * captured in a CUDA graph.  A pool has at most 2^20 pages, a table at most 2^20
+ * entries a row.  The host cannot check what lies there; a kernel
  * that meets a length outside [0, max_pages * page_size] (taken as the nearest
  * bound), a page or a parent outside its range (skipped) sets bit 64 of the
  * device status word.  Table entries behind a sequence's last page are neither
@@ -566,7 +567,8 @@ TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int3
  *         order; without it one SM reads them all.  16-byte aligned, any
  *         contents.  TG_ERR_WORKSPACE when smaller.  Calls that share a workspace
  *         must not overlap on the GPU.
- *   head_dim 64 or 128, n_q_heads <= 512; q, k_pages, v_pages and out 16-byte aligned.
+ *   head_dim 64 or 128, n_q_heads <= 512, batch * max_pages * page_size <= 2^36;
+ *   q, k_pages, v_pages and out 16-byte aligned.
  */
 TG_API tg_status tg_paged_attention(const void* q, const void* k_pages, const void* v_pages,
                                     tg_dtype dtype, int32_t batch, int32_t n_q_heads,
@@ -653,7 +655,8 @@ TG_API tg_status tg_cache_copy_pages(const tg_page_pool* pools, int32_t n_pools,
  *   k, v      device [rows, n_kv_heads, head_dim];  logsig device [rows] fp32, or
  *             NULL for 0 (a generated token); logsig_pages NULL: no log-gates
  *   cu_new    device [batch + 1], start device [batch] (of tg_cache_update)
- *   head_dim * element size a multiple of 16 bytes, 16-byte aligned k, v and pages.
+ *   head_dim * element size a multiple of 16 bytes, 16-byte aligned k, v and pages;
+ *   the rows may not lie in the pages.
  */
 TG_API tg_status tg_cache_append(const void* k, const void* v, const float* logsig, tg_dtype dtype,
                                  int64_t rows, int32_t batch, const int32_t* cu_new,
@@ -672,7 +675,8 @@ TG_API tg_status tg_cache_append(const void* k, const void* v, const float* logs
  *   state_in  [n_states, n_heads, head_dim (v), head_dim (k)] fp32
  *   state_out [batch, n_heads, head_dim, head_dim] fp32; may be state_in when
  *             parent is NULL, may not overlap it otherwise
- *   head_dim 64 or 128; q, k, v, state_in, state_out 16-byte aligned.
+ *   head_dim 64 or 128; q, k, v, state_in, state_out 16-byte aligned; no other
+ *   buffers may overlap.
  */
 TG_API tg_status tg_gated_delta_step(const void* q, const void* k, const void* v, tg_dtype dtype,
                                      const float* log_alpha, const float* beta, int32_t batch,
@@ -695,7 +699,8 @@ TG_API tg_status tg_gated_delta_step(const void* q, const void* k, const void* v
  *   scores_out [n_groups, n_out] fp32 in order, parent_out int32 the row r (the
  *   parent of tg_cache_update and tg_gated_delta_step), token_out int32; places
  *   that no candidate is left for get -inf, -1, -1.
- *   beams 1 .. TG_MAX_BEAMS, n_out 1 .. 2 * TG_MAX_BEAMS, vocab <= 2^20.
+ *   beams 1 .. TG_MAX_BEAMS, n_out 1 .. 2 * TG_MAX_BEAMS, vocab <= 2^20; the
+ *   outputs may not overlap each other or an input.
  *   workspace  device scratch of tg_beam_select_workspace_bytes, 16-byte aligned
  *              (TG_ERR_WORKSPACE when smaller); calls that share it must not
  *              overlap on the GPU.

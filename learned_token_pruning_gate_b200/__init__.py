@@ -796,24 +796,25 @@ def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=No
     the device; logsig_pages [P, page] or None (no bias); gain (None: 1), temp (None: 1) [Hq].
     workspace: "auto" (allocate one), None (no split), or paged_attention_workspace(...), which a
     decoding loop keeps.  Returns (out [B, Hq, d], lse [Hq, B] or None)."""
-    dt, i, f32 = q.dtype, q.get_device(), torch.float32
-    shape, pool = q.shape, k_pages.shape
-    if workspace is not None and not isinstance(workspace, str):
-        _workspace(workspace, q.device)
-    if not (i >= 0 and len(shape) == 3 and len(pool) == 4 and pool[3] == shape[2]
-            and q.is_contiguous() and pool[1] > 0 and shape[1] % pool[1] == 0
-            and _fits(k_pages, pool, dt, i) and _fits(v_pages, pool, dt, i)
-            and _fits(table, (shape[0], table.shape[-1]), torch.int32, i)
-            and _fits(lens, shape[:1], torch.int32, i)
-            and (logsig_pages is None or _fits(logsig_pages, pool[::2], f32, i))
-            and (gain is None or _fits(gain, shape[1:2], f32, i))
-            and (temp is None or _fits(temp, shape[1:2], f32, i))
-            and (out is None or _fits(out, shape, dt, i))
-            and (lse is None or _fits(lse, shape[1::-1], f32, i))):
+    dt, i, f32, i32 = q.dtype, q.get_device(), torch.float32, torch.int32
+    if q.dim() != 3 or k_pages.dim() != 4 or table.dim() != 2:
         _expect_paged_attention(q, k_pages, v_pages, table, lens, logsig_pages, gain, temp, out,
                                 lse)
-    B, Hq, dh = shape
-    P, Hkv, page, _ = pool
+    B, Hq, dh = q.shape
+    P, Hkv, page, d = pool = k_pages.shape
+    max_pages = table.shape[1]
+    if workspace is not None and not isinstance(workspace, str):
+        _workspace(workspace, q.device)
+    if not (i >= 0 and d == dh and Hkv > 0 and Hq % Hkv == 0 and q.is_contiguous()
+            and _fits(k_pages, pool, dt, i) and _fits(v_pages, pool, dt, i)
+            and _fits(table, (B, max_pages), i32, i) and _fits(lens, (B,), i32, i)
+            and (logsig_pages is None or _fits(logsig_pages, (P, page), f32, i))
+            and (gain is None or _fits(gain, (Hq,), f32, i))
+            and (temp is None or _fits(temp, (Hq,), f32, i))
+            and (out is None or _fits(out, (B, Hq, dh), dt, i))
+            and (lse is None or _fits(lse, (Hq, B), f32, i))):
+        _expect_paged_attention(q, k_pages, v_pages, table, lens, logsig_pages, gain, temp, out,
+                                lse)
     with _on(i):
         one = torch.ones(Hq, device=q.device) if gain is None or temp is None else None
         gain = one if gain is None else gain
@@ -827,7 +828,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=No
         ws_bytes = 0 if workspace is None else workspace.numel()
         _check("tg_paged_attention", library().tg_paged_attention(
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _dtype_code(q), B, Hq, Hkv, dh,
-            P, page, table.data_ptr(), table.shape[1], lens.data_ptr(), _addr(logsig_pages),
+            P, page, table.data_ptr(), max_pages, lens.data_ptr(), _addr(logsig_pages),
             gain.data_ptr(), temp.data_ptr(), out.data_ptr(), _addr(lse),
             workspace.data_ptr() if ws_bytes else None, ws_bytes, _raw_stream(i)))
     return out, lse
@@ -862,19 +863,20 @@ def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_o
     where the sequence did not grow), and copy_src, copy_dst [B'], the page copies for
     cache_copy_pages that have to run before anything is appended."""
     i, i32 = table.get_device(), torch.int32
-    shape, P = table.shape, refs.shape[0]
-    Bo = shape[0] if parent is None else parent.shape[0]
+    if table.dim() != 2:
+        _expect_table(table, lens, table.device)
+    B, mp = table.shape
+    P = refs.shape[0]
+    Bo = B if parent is None else parent.shape[0]
     small = (lens_out, start, copy_src, copy_dst)
-    if not (i >= 0 and len(shape) == 2 and _fits(table, shape, i32, i)
-            and _fits(lens, shape[:1], i32, i) and _fits(refs, (P,), i32, i)
-            and (parent is None or _fits(parent, (Bo,), i32, i))
+    if not (i >= 0 and _fits(table, (B, mp), i32, i) and _fits(lens, (B,), i32, i)
+            and _fits(refs, (P,), i32, i) and (parent is None or _fits(parent, (Bo,), i32, i))
             and (cu_new is None or _fits(cu_new, (Bo + 1,), i32, i))
-            and (table_out is None or _fits(table_out, (Bo, shape[1]), i32, i))
+            and (table_out is None or _fits(table_out, (Bo, mp), i32, i))
             and (refs_out is None or _fits(refs_out, (P,), i32, i))
             and all(t is None or _fits(t, (Bo,), i32, i) for t in small)):
         _expect_cache_update(table, lens, refs, parent, cu_new, table_out, lens_out, refs_out,
                              start, copy_src, copy_dst)
-    B, mp = shape
     with _on(i):
         if table_out is None:
             table_out = torch.full((Bo, mp), -1, dtype=i32, device=table.device)
@@ -1025,23 +1027,25 @@ def gated_delta_step(q, k, v, log_alpha, beta, state, parent=None, eps=1e-6, out
     starts from state[b], and state_out=state updates in place.
     Returns (out [B, H, d], state_out [B, H, d, d])."""
     i, f32, dt = q.get_device(), torch.float32, q.dtype
-    shape, S = q.shape, state.shape[0]
-    full = shape + shape[-1:]  # [B, H, d, d]
-    if not (i >= 0 and len(shape) == 3 and q.is_contiguous() and _fits(k, shape, dt, i)
-            and _fits(v, shape, dt, i) and _fits(log_alpha, shape[:2], f32, i)
-            and _fits(beta, shape[:2], f32, i) and _fits(state, (S,) + full[1:], f32, i)
-            and (parent is None or _fits(parent, shape[:1], torch.int32, i))
+    if q.dim() != 3 or state.dim() != 4:
+        _expect_delta_step(q, k, v, log_alpha, beta, state, parent, out, state_out)
+    B, H, d = shape = q.shape
+    S = state.shape[0]
+    if not (i >= 0 and q.is_contiguous() and _fits(k, shape, dt, i) and _fits(v, shape, dt, i)
+            and _fits(log_alpha, (B, H), f32, i) and _fits(beta, (B, H), f32, i)
+            and _fits(state, (S, H, d, d), f32, i)
+            and (parent is None or _fits(parent, (B,), torch.int32, i))
             and (out is None or _fits(out, shape, dt, i))
-            and (state_out is None or _fits(state_out, full, f32, i))
-            and (parent is not None or S >= shape[0])):
+            and (state_out is None or _fits(state_out, (B, H, d, d), f32, i))
+            and (parent is not None or S >= B)):
         _expect_delta_step(q, k, v, log_alpha, beta, state, parent, out, state_out)
     with _on(i):
         out = torch.empty_like(q) if out is None else out
         if state_out is None:
-            state_out = torch.empty(full, dtype=f32, device=q.device)
+            state_out = torch.empty((B, H, d, d), dtype=f32, device=q.device)
         _check("tg_gated_delta_step", library().tg_gated_delta_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), log_alpha.data_ptr(),
-            beta.data_ptr(), shape[0], shape[1], shape[2], eps, state.data_ptr(), S,
+            beta.data_ptr(), B, H, d, eps, state.data_ptr(), S,
             _addr(parent), state_out.data_ptr(), out.data_ptr(), _raw_stream(i)))
     return out, state_out
 

@@ -93,6 +93,10 @@ tg_status tg_paged_attention(const void* q, const void* k_pages, const void* v_p
   if (r != TG_OK || (r = check_batch(batch, "batch")) != TG_OK ||
       (r = check_pages(n_pages, page_size, max_pages, &a.page_shift)) != TG_OK)
     return r;
+  // (the kernel counts tiles of at least 64 keys in 32 bits)
+  if (static_cast<int64_t>(batch) * max_pages * page_size > (int64_t{1} << 36))
+    return set_error(TG_ERR_UNSUPPORTED, "batch x max_pages x page_size = %lld exceeds 2^36",
+                     static_cast<long long>(static_cast<int64_t>(batch) * max_pages * page_size));
   if (batch == 0) return TG_OK;
   if (!q || !lens || !gain || !temp || !out || (max_pages > 0 && !table) ||
       (n_pages > 0 && (!k_pages || !v_pages)))
@@ -255,6 +259,14 @@ tg_status tg_cache_append(const void* k, const void* v, const float* logsig, tg_
     return set_error(TG_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages))
     return set_error(TG_ERR_ALIGNMENT, "k, v, k_pages and v_pages must be 16-byte aligned");
+  const size_t row_bytes = static_cast<size_t>(rows) * n_kv_heads * head_dim * esz;
+  const size_t pool_bytes = static_cast<size_t>(n_pages) * page_size * n_kv_heads * head_dim * esz;
+  const size_t gate_bytes = logsig_pages ? 4 * static_cast<size_t>(n_pages) * page_size : 0;
+  const Span in[] = {{k, row_bytes, "k"}, {v, row_bytes, "v"}, {logsig, 4 * static_cast<size_t>(rows), "logsig"}};
+  const Span out[] = {{k_pages, pool_bytes, "k_pages"}, {v_pages, pool_bytes, "v_pages"},
+                      {logsig_pages, gate_bytes, "logsig_pages"}};
+  const int same[] = {-1, -1, -1};
+  if ((r = check_spans(in, 3, out, 3, same)) != TG_OK) return r;
   if ((r = status_word(&a.status)) != TG_OK) return r;
   a.k = k;
   a.v = v;
@@ -296,12 +308,17 @@ tg_status tg_gated_delta_step(const void* q, const void* k, const void* v, tg_dt
     return set_error(TG_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state_in) || !aligned16(state_out))
     return set_error(TG_ERR_ALIGNMENT, "q, k, v, state_in and state_out must be 16-byte aligned");
-  const size_t one = 4 * static_cast<size_t>(n_heads) * head_dim * head_dim;
-  if (overlap(state_in, one * n_states, state_out, one * batch) && (parent || state_in != state_out))
-    return set_error(TG_ERR_INVALID_ARG, "state_out overlaps state_in");
-  uint32_t* status = nullptr;
-  tg_status r = status_word(&status);
+  const size_t heads = static_cast<size_t>(batch) * n_heads, one = 4 * static_cast<size_t>(n_heads) * head_dim * head_dim;
+  const size_t row_bytes = heads * head_dim * (dtype == TG_BF16 ? 2 : 4);
+  const Span in[] = {{state_in, one * n_states, "state_in"}, {q, row_bytes, "q"}, {k, row_bytes, "k"},
+                     {v, row_bytes, "v"}, {log_alpha, 4 * heads, "log_alpha"}, {beta, 4 * heads, "beta"},
+                     {parent, 4 * static_cast<size_t>(batch), "parent"}};
+  const Span outs[] = {{state_out, one * batch, "state_out"}, {out, row_bytes, "out"}};
+  const int same[] = {parent ? -1 : 0, -1};
+  tg_status r = check_spans(in, 7, outs, 2, same);
   if (r != TG_OK) return r;
+  uint32_t* status = nullptr;
+  if ((r = status_word(&status)) != TG_OK) return r;
   return launch_delta_step(q, k, v, dtype, log_alpha, beta, batch, n_heads, head_dim, eps, state_in,
                            n_states, parent, state_out, out, status,
                            reinterpret_cast<cudaStream_t>(stream));
@@ -346,6 +363,12 @@ tg_status tg_beam_select(const void* logits, tg_dtype dtype, const float* scores
                      workspace ? workspace_bytes : 0, need);
   if (!aligned16(logits) || !aligned16(workspace))
     return set_error(TG_ERR_ALIGNMENT, "logits and workspace must be 16-byte aligned");
+  const size_t rows = static_cast<size_t>(n_groups) * beams, picks = 4 * static_cast<size_t>(n_groups) * n_out;
+  const Span in[] = {{logits, rows * vocab * (dtype == TG_BF16 ? 2 : 4), "logits"}, {scores, 4 * rows, "scores"}};
+  const Span out[] = {{scores_out, picks, "scores_out"}, {parent_out, picks, "parent_out"},
+                      {token_out, picks, "token_out"}, {workspace, need, "workspace"}};
+  const int same[] = {-1, -1, -1, -1};
+  if ((r = check_spans(in, 2, out, 4, same)) != TG_OK) return r;
   return launch_beam_select(logits, dtype, scores, n_groups, beams, vocab, n_out, scores_out, parent_out,
                             token_out, workspace, reinterpret_cast<cudaStream_t>(stream));
 }

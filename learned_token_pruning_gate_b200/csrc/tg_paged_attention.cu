@@ -470,6 +470,11 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = u;
 }
 
+// a / b for 0 <= a, 0 < b; a 64-bit division takes ten times as long.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return a <= UINT32_MAX ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 // A place in the list of tiles: tile j of unit u of sequence b.
 struct Place {
   int32_t b, u, j, tiles;  // tiles of every unit of the sequence
@@ -493,45 +498,62 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool bad = false;
 
-  // tiles of every sequence, scanned: a run of sequences per thread
+  // Everything that does not depend on anything else is requested at once.
   const int batch = p.a.batch;
-  const int run = (batch + kThreads - 1) / kThreads;
   const int64_t most = static_cast<int64_t>(p.a.max_pages) << p.a.page_shift;
-  for (int h = tid; h < p.a.hq; h += kThreads)
-    heads[h] = make_float2(1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h]), p.a.gain[h]);
-  int sum = 0;
-  for (int i = 0; i < run; ++i) {
-    const int b = tid * run + i;
-    if (b >= batch) break;
-    int len = p.a.lens[b];
-    if (len < 0 || len > most) {
-      bad = true;
-      len = len < 0 ? 0 : static_cast<int>(most);
-    }
-    lens[b] = len;
-    sum += (len + kTile - 1) / kTile;
-    ends[b] = sum;
-  }
-  int scan = sum;
+  auto checked = [&](int len) {
+    if (len >= 0 && len <= most) return len;
+    bad = true;
+    return len < 0 ? 0 : static_cast<int>(most);
+  };
+  const float temp0 = tid < p.a.hq ? p.a.temp[tid] : 1.0f, gain0 = tid < p.a.hq ? p.a.gain[tid] : 0.0f;
+  // The tiles of every sequence, scanned.  Up to 32 sequences every warp does for itself; more are
+  // shared among the threads, a run of them each.
+  if (batch <= 32) {
+    const int len = lane < batch ? checked(p.a.lens[lane]) : 0;
+    int scan = (len + kTile - 1) / kTile;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += y;
+    }
+    if (lane < batch) {  // (the same values from every warp)
+      lens[lane] = len;
+      ends[lane] = scan;
+    }
+    __syncwarp();
+  } else {
+    const int run = (batch + kThreads - 1) / kThreads;
+    int sum = 0;
+    for (int i = 0; i < run; ++i) {
+      const int b = tid * run + i;
+      if (b >= batch) break;
+      const int len = checked(p.a.lens[b]);
+      lens[b] = len;
+      sum += (len + kTile - 1) / kTile;
+      ends[b] = sum;
+    }
+    int scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += y;
+    }
+    if (lane == 31) warp_sums[warp] = scan;
+    __syncthreads();
+    int before = scan - sum;
+    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+    for (int i = 0; i < run; ++i) {
+      const int b = tid * run + i;
+      if (b >= batch) break;
+      ends[b] += before;
+    }
+    __syncthreads();
   }
-  if (lane == 31) warp_sums[warp] = scan;
-  __syncthreads();
-  int before = scan - sum;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
-  for (int i = 0; i < run; ++i) {
-    const int b = tid * run + i;
-    if (b >= batch) break;
-    ends[b] += before;
-  }
-  __syncthreads();
 
   // this CTA's run of the list: an equal share with a workspace, whole units without
   const int64_t total = static_cast<int64_t>(ends[batch - 1]) * p.units;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t per = quotient(total + gridDim.x - 1, static_cast<int>(gridDim.x));
   int64_t at = min(total, per * blockIdx.x), end = min(total, at + per);
   if (!p.shares) {
     const int64_t units = static_cast<int64_t>(batch) * p.units, share = (units + gridDim.x - 1) / gridDim.x;
@@ -545,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
   }
 
   auto heads_of = [&](int u, int* hk, int* h0, int* nh) {
-    *hk = u / p.blocks;
+    *hk = p.blocks == 1 ? u : u / p.blocks;
     const int block = u - *hk * p.blocks;
     *h0 = *hk * p.group + block * H;
     *nh = min(H, p.group - block * H);
@@ -601,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
       const int64_t in_seq = at - static_cast<int64_t>(first) * p.units;
       now.b = lo;
       now.tiles = ends[lo] - first;
-      now.u = static_cast<int>(in_seq / now.tiles);
+      now.u = static_cast<int>(quotient(in_seq, now.tiles));
       now.j = static_cast<int>(in_seq - static_cast<int64_t>(now.u) * now.tiles);
     }
     int hk, h0, nh;
@@ -612,6 +634,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
     core.load_k(p, keys, 0);
     core.load_v(p, keys, 0);
     core.load_q(p, now.b, h0, nh);
+    if (tid < p.a.hq) heads[tid] = make_float2(1.0f / (sqrtf(static_cast<float>(D)) * temp0), gain0);
+    for (int h = tid + kThreads; h < p.a.hq; h += kThreads)
+      heads[h] = make_float2(1.0f / (sqrtf(static_cast<float>(D)) * p.a.temp[h]), p.a.gain[h]);
+    __syncthreads();
     core.begin(heads + h0, nh);
     int j0 = now.j;  // where the present unit was entered
     for (;; ++at) {
@@ -653,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
         if (j0 == 0 && p.shares && tid == 0) {
           const int64_t last = at - now.j + now.tiles - 1;  // the unit's last tile
           p.shares[static_cast<int64_t>(now.b) * p.units + now.u] =
-              whole ? make_int2(0, -1) : make_int2(blockIdx.x, static_cast<int>(last / per));
+              whole ? make_int2(0, -1) : make_int2(blockIdx.x, static_cast<int>(quotient(last, static_cast<int>(per))));
         }
         if (!more) break;
         core.begin(heads + next_h0, next_nh);

@@ -152,6 +152,7 @@ def test_paged_attention_refusals(L):
     for kw in (dict(q=ODD), dict(k=ODD), dict(v=ODD), dict(out=ODD)):
         assert call(**kw) == ALIGN, kw
     assert call(B=0, q=None) == OK
+    assert call(B=1024, page=128, mp=2 ** 20) == UNSUP
     n = ctypes.c_size_t(7)
     assert L.tg_paged_attention_workspace_bytes(0, 2, 5, 2, 64, ctypes.byref(n)) == SHAPE and n.value == 0
     assert L.tg_paged_attention_workspace_bytes(0, 2, 4, 2, 64, None) == INVALID
@@ -211,6 +212,8 @@ def test_cache_refusals(L):
     for kw in (dict(k=None), dict(v=None), dict(cu=None), dict(st=None), dict(t=None), dict(kp=None), dict(vp=None),
                dict(rows=-1), dict(rows=2 ** 31)):
         assert append(**kw) == INVALID, kw
+    for kw in (dict(kp=_p(0)), dict(vp=_p(1)), dict(vp=_p(5)), dict(vp=ctypes.c_void_p(_p(0).value + 256))):
+        assert append(**kw) == INVALID and b"overlap" in L.tg_last_error_message(), kw
     assert append(kp=ODD) == ALIGN and append(page=100) == UNSUP and append(rows=0) == OK
 
 
@@ -224,6 +227,8 @@ def test_delta_step_refusals(L):
                dict(la=None), dict(be=None), dict(s=None), dict(so_=None), dict(out=None), dict(parent=_p(8), so_=_p(5)),
                dict(so_=ctypes.c_void_p(_p(5).value + 16))):
         assert call(**kw) == INVALID, kw
+    for kw in (dict(out=_p(0)), dict(out=_p(2)), dict(out=_p(5)), dict(out=_p(6)), dict(so_=_p(1)), dict(parent=_p(7))):
+        assert call(**kw) == INVALID and b"overlap" in L.tg_last_error_message(), kw
     assert call(q=ODD) == ALIGN and call(s=ODD) == ALIGN and call(so_=ODD) == ALIGN
     assert call(B=0, q=None) == OK
 
@@ -236,6 +241,8 @@ def test_beam_select_refusals(L):
     assert call(beams=33) == UNSUP and call(n=65) == UNSUP and call(V=2 ** 20 + 1) == UNSUP and call(G=2 ** 20) == UNSUP
     for kw in (dict(x=None), dict(s=None), dict(so_=None), dict(p=None), dict(t=None)):
         assert call(**kw) == INVALID, kw
+    for kw in (dict(so_=_p(1)), dict(p=_p(2)), dict(t=_p(0)), dict(ws=_p(0)), dict(ws=_p(3))):
+        assert call(**kw) == INVALID and b"overlap" in L.tg_last_error_message(), kw
     assert call(ws=None) == WORKSPACE and call(nb=16) == WORKSPACE
     assert call(x=ODD) == ALIGN and call(ws=ODD) == ALIGN
     assert call(G=0, x=None) == OK

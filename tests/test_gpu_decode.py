@@ -144,6 +144,9 @@ def test_attention_defaults_and_workspace_reuse():
         alone = tg.paged_attention(d["q"][:1], d["k_pages"], d["v_pages"], d["table"][:1], d["lens"][:1],
                                    workspace=ws)[0]
         assert_close("one sequence alone", host_f32(alone), host_f32(out[:1]), 1e-5, 2.0 ** -7)
+    inplace = d["q"].clone()
+    tg.paged_attention(inplace, d["k_pages"], d["v_pages"], d["table"], d["lens"], workspace=ws, out=inplace)
+    assert torch.equal(inplace, out)
     first = tg.paged_attention(d["q"], d["k_pages"], d["v_pages"], d["table"], d["lens"], workspace=ws)[0]
     assert torch.equal(first, out)
 
@@ -522,6 +525,24 @@ def test_beam_select_ties_and_missing(dtype):
     assert got[2].tolist() == [[3, 4, 7, -1, -1]]
     scores[:] = float("nan")
     assert tg.beam_select(dev(x), dev(scores), 2)[1].tolist() == [[-1, -1]]
+
+
+def test_beam_select_largest():
+    """The largest sizes: 32 beams of 2^20 logits, 64 candidates; and many groups of one beam."""
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn((32, 2 ** 20), generator=g, device="cuda") * 2.0
+    scores = -torch.rand((1, 32), generator=g, device="cuda")
+    best, parent, token = tg.beam_select(x, scores, 64)
+    total = (x.double() - torch.logsumexp(x.double(), 1, keepdim=True) + scores.double().T).reshape(-1)
+    want = torch.topk(total, 64)
+    assert torch.equal(parent[0].long() * 2 ** 20 + token[0], want.indices)  # (random fp32: no two are equal)
+    assert_close("scores", best[0].cpu().numpy(), want.values.cpu().numpy(), 1e-6, 2.0 ** -23)
+    x = torch.randn((3000, 33), generator=g, device="cuda").bfloat16()
+    best, parent, token = tg.beam_select(x, torch.zeros((3000, 1), device="cuda"), 1)
+    assert torch.equal(parent[:, 0].cpu(), torch.arange(3000, dtype=torch.int32))
+    first = (x == x.amax(1, keepdim=True)).float().argmax(1)
+    assert torch.equal(x.gather(1, token.long()), x.amax(1, keepdim=True))
+    assert (token[:, 0] <= first).all()
 
 
 def test_beam_select_sorted_rows():
