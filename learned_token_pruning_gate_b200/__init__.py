@@ -869,23 +869,23 @@ def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_o
     P = refs.shape[0]
     Bo = B if parent is None else parent.shape[0]
     small = (lens_out, start, copy_src, copy_dst)
+    given = [t for t in small if t is not None]
     if not (i >= 0 and _fits(table, (B, mp), i32, i) and _fits(lens, (B,), i32, i)
             and _fits(refs, (P,), i32, i) and (parent is None or _fits(parent, (Bo,), i32, i))
             and (cu_new is None or _fits(cu_new, (Bo + 1,), i32, i))
             and (table_out is None or _fits(table_out, (Bo, mp), i32, i))
             and (refs_out is None or _fits(refs_out, (P,), i32, i))
-            and all(t is None or _fits(t, (Bo,), i32, i) for t in small)):
+            and all([_fits(t, (Bo,), i32, i) for t in given])):
         _expect_cache_update(table, lens, refs, parent, cu_new, table_out, lens_out, refs_out,
                              start, copy_src, copy_dst)
     with _on(i):
         if table_out is None:
             table_out = torch.full((Bo, mp), -1, dtype=i32, device=table.device)
         refs_out = torch.empty_like(refs) if refs_out is None else refs_out
-        if lens_out is None or start is None or copy_src is None or copy_dst is None:
-            # one allocation for those that are not given
+        if len(given) < 4:  # one allocation for those that are not given
             fresh = torch.empty((4, Bo), dtype=i32, device=table.device).unbind()
-            lens_out, start, copy_src, copy_dst = [f if t is None else t
-                                                   for f, t in zip(fresh, small)]
+            small = fresh if not given else [f if t is None else t for f, t in zip(fresh, small)]
+        lens_out, start, copy_src, copy_dst = small
         _check("tg_cache_update", library().tg_cache_update(
             table.data_ptr(), lens.data_ptr(), B, refs.data_ptr(), P, page_size, mp,
             _addr(parent), Bo, _addr(cu_new), table_out.data_ptr(), lens_out.data_ptr(),

@@ -217,6 +217,27 @@ def test_attention_repeats_and_replays():
     assert_close("replayed", host_f32(out), host_f32(eager), 1e-6, 2.0 ** -7)
 
 
+def test_attention_on_two_streams():
+    """Two calls at once, each with its own workspace, beside a third one's kernels."""
+    ps = [gen.paged_inputs(lens, 16, 8, 128, 64, 20 + i) for i, lens in enumerate(([2000, 33, 900], [5, 3000]))]
+    ds = [{n: dev(t) for n, t in p.items()} for p in ps]
+    wss = [tg.paged_attention_workspace(len(p["lens"]), 16, 8, 128) for p in ps]
+    outs = [[torch.empty_like(d["q"]) for _ in range(20)] for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for d, ws, o, s in zip(ds, wss, outs, streams):
+            with torch.cuda.stream(s):
+                tg.paged_attention(d["q"], d["k_pages"], d["v_pages"], d["table"], d["lens"], d["logsig_pages"],
+                                   d["gain"], d["temp"], out=o[i], workspace=ws)
+    torch.cuda.synchronize()
+    for p, d, o in zip(ps, ds, outs):
+        want, lse = tg.paged_attention(d["q"], d["k_pages"], d["v_pages"], d["table"], d["lens"], d["logsig_pages"],
+                                       d["gain"], d["temp"], want_lse=True)
+        _check_attention(p, want, lse)
+        assert all(torch.equal(x, want) for x in o)
+
+
 def test_attention_far_pages():
     """Offsets past 2^31 elements and 2^32 bytes: the last pages of a pool of 5 GB."""
     P, Hkv, page, d = 9000, 8, 128, 128
