@@ -20,7 +20,6 @@ from __future__ import annotations
 import collections
 import contextlib
 import ctypes
-import math
 import os
 
 import numpy as np
@@ -951,8 +950,8 @@ def cache_copy_pages(pools, copy_src, copy_dst, count=None):
             raise ValueError(f"pools: {tuple(shape)} on {t.device}, expected contiguous "
                              f"[layers, {P}, ...] on {copy_src.device}")
         a.base = t.data_ptr()
-        a.page_bytes = math.prod(shape[2:]) * t.element_size()
         a.layers = shape[0]
+        a.page_bytes = t.nbytes // (shape[0] * P) if t.nbytes else 16
     _need_cuda(copy_src)
     if not pools:
         return

@@ -15,6 +15,14 @@
 // matter.  A chunk finds its threshold by bisection over the threads' maxima, one
 // barrier with a count per step; it stops as soon as the count is close to n.
 //
+// What bounds them: the chunk kernel its instructions (about 450 a thread for 64
+// logits; the exponentials alone are 2.8 us of the special-function units for 96
+// rows of 131071) and its barriers, the merge the chain of dependent steps of one
+// CTA per group (log-sums in 64 bits 1.4 us, rankings 3 us).  96 rows of 131071
+// bf16 logits take 18.2 us on the device (HBM floor 3.9), 4 rows of 32000 fp32
+// 7.1 us.  Finding a chunk's threshold by comparing every thread's maximum with
+// every other's took 48 us instead of 10 for the chunks.
+//
 // The scores are compared in 64 bits: beams meet at sums that differ in the last
 // places of 32, and a chunk's sum in 32 bits (at most 64 terms per thread, then a tree)
 // is off by less than 1e-7 of itself.

@@ -2,22 +2,26 @@
 // compaction, page copies and appended rows.
 //
 // The table kernels are integer work on a few hundred kilobytes that later steps
-// depend on, so what counts is how often they cross the device: one cluster of
-// eight CTAs does all phases of a call in one launch, with cluster barriers
-// between the phases in place of launches, and every CTA computes the scans over
-// the (at most 1024) sequences for itself.  Counts are integers, so the atomic
-// updates give the same result in any order.  Reference counts and tables that
-// other CTAs of the cluster write are read through L2 (__ldcg).
+// depend on, so what bounds them is the chain of dependent accesses and barriers:
+// one launch does all phases of a call, in one CTA or in a cluster of eight with
+// cluster barriers between the phases, and every CTA computes the scans over the
+// (at most 1024) sequences for itself.  Counts are integers, so the atomic updates
+// give the same result in any order.  Reference counts and tables that other CTAs
+// of the cluster write are read through L2 (__ldcg).  A beam search's step of 32
+// sequences of 70 pages in a pool of 2048 (fork, growth, page copies of 4 layers)
+// takes 11.7 us on the device.
 //
-// The data kernels (page copies, appended rows) are plain 16-byte streams.
+// The data kernels (page copies, appended rows) are 16-byte streams bound by HBM:
+// 343 MB of a compaction move at the copy rate (49.5 us, 6.9 TB/s).
 #include "tg_internal.cuh"
 
 namespace tg {
 namespace {
 
-constexpr int kTabCtas = 8;
+constexpr int kMaxTabCtas = 8;
 constexpr int kTabThreads = 1024;
 constexpr int kTabWarps = kTabThreads / 32;
+constexpr int kPiece = 128;  // table entries a warp has in flight
 static_assert(kTabThreads >= kMaxSeqs, "a thread per sequence");
 
 // Inclusive scan over the block's threads; `warp_sums` holds 32 words and may be
@@ -42,12 +46,36 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int* total) {
   return warp > 0 ? x + before : x;
 }
 
-// Writes v into word `slot` of the array at the same place in every CTA of the cluster.
-__device__ __forceinline__ void publish(int* array, int slot, int v) {
-  const uint32_t at = smem_u32(array + slot);
-  for (uint32_t r = 0; r < kTabCtas; ++r)
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(at, r)), "r"(v) : "memory");
+// The largest x of the block; `warp_max` holds 32 words.
+__device__ __forceinline__ int block_max(int x, int* warp_max) {
+  x = __reduce_max_sync(0xffffffffu, x);
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = __reduce_max_sync(0xffffffffu, warp_max[threadIdx.x & 31]);
+  __syncthreads();
+  return x;
 }
+
+// The CTAs of a table call: a cluster, or one CTA alone, whose barriers are an order cheaper.
+template <int kCtas>
+struct Team {
+  static __device__ __forceinline__ int rank() { return kCtas == 1 ? 0 : static_cast<int>(cluster_ctarank()); }
+  // all threads of the team; global and shared memory written before is seen after it
+  static __device__ __forceinline__ void sync() {
+    if constexpr (kCtas == 1) __syncthreads();
+    else cluster_sync_all();
+  }
+  // writes v into word `slot` of the array at the same place in every CTA
+  static __device__ __forceinline__ void publish(int* array, int slot, int v) {
+    if constexpr (kCtas == 1) {
+      array[slot] = v;
+    } else {
+      const uint32_t at = smem_u32(array + slot);
+      for (uint32_t r = 0; r < kCtas; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(at, r)), "r"(v) : "memory");
+    }
+  }
+};
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int shift) {
   return static_cast<int>((tokens + (int64_t{1} << shift) - 1) >> shift);
@@ -68,15 +96,18 @@ __device__ __forceinline__ int checked_len(int len, int max_pages, int shift, bo
 }
 
 // ---- fork, free and growth ---------------------------------------------------------------------
-__global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
-    cache_update_kernel(const CacheUpdateArgs a) {
+template <int kTabCtas>
+__global__ void __launch_bounds__(kTabThreads) cache_update_kernel(const __grid_constant__ CacheUpdateArgs a) {
+  using Team = Team<kTabCtas>;
   __shared__ int kids[kMaxSeqs];    // output sequences per input sequence
-  __shared__ int shared_page[kMaxSeqs];  // the partly filled page a growing sequence shares, or -1
+  __shared__ int in_pages[kMaxSeqs];  // pages of every input sequence
+  __shared__ int from_seq[kMaxSeqs];  // the input sequence of every output sequence, or -1
+  __shared__ __align__(16) int shared_page[kMaxSeqs];  // the partly filled page a growing sequence shares, or -1
   __shared__ int ends[kMaxSeqs];    // inclusive scan of the pages that sequences need
   __shared__ int firsts[kMaxSeqs];  // 2 x the table slot of the first page a sequence gets, + 1 for a copy
   __shared__ int sums[32], sums2[32], free_count[kTabCtas];
   const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = Team::rank();
   const int gwarp = rank * kTabWarps + (tid >> 5);
   constexpr int kWarps = kTabCtas * kTabWarps;
   const int page = 1 << a.page_shift;
@@ -87,32 +118,40 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
   // children per input sequence; the output sequence of this thread
   kids[tid] = a.parent ? 0 : 1;
   __syncthreads();
-  int held = 0;  // tokens of output sequence tid
-  if (tid < a.batch_out) {
-    int from = tid;
-    if (a.parent) {
-      from = a.parent[tid];
-      if (from < -1 || from >= a.batch_in) {
-        bad = true;
-        from = -1;
-      }
-      if (from >= 0) atomicAdd(&kids[from], 1);
+  int from = tid < a.batch_out ? tid : -1;
+  if (tid < a.batch_out && a.parent) {
+    from = a.parent[tid];
+    if (from < -1 || from >= a.batch_in) {
+      bad = true;
+      from = -1;
     }
-    if (from >= 0) held = checked_len(a.lens_in[from], a.max_pages, a.page_shift, &bad);
+    if (from >= 0) atomicAdd(&kids[from], 1);
   }
+  from_seq[tid] = from;
+  const int mine_in =
+      tid < a.batch_in ? pages_of(checked_len(a.lens_in[tid], a.max_pages, a.page_shift, &bad), a.page_shift) : 0;
+  in_pages[tid] = mine_in;
+  const int longest = block_max(mine_in, sums);
+  // tokens of output sequence tid
+  const int held = from >= 0 ? checked_len(a.lens_in[from], a.max_pages, a.page_shift, &bad) : 0;
   if (a.refs_out != a.refs_in)
     for (int p = rank * kTabThreads + tid; p < a.n_pages; p += kTabCtas * kTabThreads)
       a.refs_out[p] = a.refs_in[p];
-  cluster_sync_all();
+  Team::sync();
 
-  // the counts follow the children; the tables follow the parents
+  // The counts follow the children; the tables follow the parents.  A warp takes kPiece entries of
+  // a row at a time, the longest row setting how many pieces there are.
+  const int pieces = (longest + kPiece - 1) / kPiece;
   if (a.parent) {
-    for (int b = gwarp; b < a.batch_in; b += kWarps) {
-      const int change = kids[b] - 1;
+    for (int64_t w = gwarp; w < static_cast<int64_t>(a.batch_in) * pieces; w += kWarps) {
+      const int b = static_cast<int>(w / pieces), j0 = static_cast<int>(w - static_cast<int64_t>(b) * pieces) * kPiece;
+      const int change = kids[b] - 1, used = in_pages[b];
       if (change == 0) continue;
-      const int used = pages_of(checked_len(a.lens_in[b], a.max_pages, a.page_shift, &bad), a.page_shift);
       const int32_t* row = a.table_in + static_cast<int64_t>(b) * a.max_pages;
-      for (int j = lane; j < used; j += 32) {
+#pragma unroll
+      for (int u = 0; u < kPiece; u += 32) {
+        const int j = j0 + u + lane;
+        if (j >= used) continue;
         const int p = row[j];
         if (p >= 0 && p < a.n_pages) atomicAdd(a.refs_out + p, change);
         else bad = true;
@@ -120,16 +159,23 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
     }
   }
   if (a.table_out != a.table_in) {
-    for (int i = gwarp; i < a.batch_out; i += kWarps) {
-      const int from = a.parent ? a.parent[i] : i;
-      if (from < 0 || from >= a.batch_in) continue;
-      const int used = pages_of(checked_len(a.lens_in[from], a.max_pages, a.page_shift, &bad), a.page_shift);
-      const int32_t* row = a.table_in + static_cast<int64_t>(from) * a.max_pages;
-      int32_t* dst = a.table_out + static_cast<int64_t>(i) * a.max_pages;
-      for (int j = lane; j < used; j += 32) dst[j] = row[j];
+    for (int64_t w = gwarp; w < static_cast<int64_t>(a.batch_out) * pieces; w += kWarps) {
+      const int i = static_cast<int>(w / pieces), j0 = static_cast<int>(w - static_cast<int64_t>(i) * pieces) * kPiece;
+      const int source = from_seq[i];
+      if (source < 0) continue;
+      const int used = in_pages[source];
+      const int32_t* row = a.table_in + static_cast<int64_t>(source) * a.max_pages + j0 + lane;
+      int32_t* dst = a.table_out + static_cast<int64_t>(i) * a.max_pages + j0 + lane;
+      int32_t x[kPiece / 32];
+#pragma unroll
+      for (int u = 0; u < kPiece / 32; ++u)
+        if (j0 + lane + 32 * u < used) x[u] = row[32 * u];
+#pragma unroll
+      for (int u = 0; u < kPiece / 32; ++u)
+        if (j0 + lane + 32 * u < used) dst[32 * u] = x[u];
     }
   }
-  cluster_sync_all();
+  Team::sync();
 
   // what each sequence needs
   int n = 0, used = 0, grown = 0, last = -1, count = 0;
@@ -167,12 +213,16 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
     for (int p = p0; p < p1; ++p) mine += __ldcg(a.refs_out + p) <= 0;
   int cta_free = 0;
   const int free_end = block_scan(mine, sums, &cta_free);  // (its barrier publishes shared_page too)
-  if (tid == 0) publish(free_count, rank, cta_free);
+  if (tid == 0) Team::publish(free_count, rank, cta_free);
   // of the holders of a shared page that grow, the last one in order keeps it if nobody else holds it
   bool copies = false;
   if (shares) {
     int before = 0;
-    for (int j = 0; j < tid; ++j) before += shared_page[j] == last;
+    for (int j = 0; j < tid >> 2; ++j) {
+      const int4 p = reinterpret_cast<const int4*>(shared_page)[j];
+      before += (p.x == last) + (p.y == last) + (p.z == last) + (p.w == last);
+    }
+    for (int j = tid & ~3; j < tid; ++j) before += shared_page[j] == last;
     copies = count - before > 1;
   }
   // (no more than n_pages + 1, which is never served, so that 1024 of them add up within 32 bits)
@@ -181,7 +231,7 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
   const int end = block_scan(need, sums2, &total_need);
   ends[tid] = end;
   firsts[tid] = copies ? 2 * (used - 1) + 1 : 2 * used;
-  cluster_sync_all();
+  Team::sync();
 
   int total_free = 0, free_before = 0;
 #pragma unroll
@@ -222,15 +272,22 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
 }
 
 // ---- compaction --------------------------------------------------------------------------------
-__global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
-    cache_compact_kernel(const CacheCompactArgs a) {
+template <int kTabCtas>
+__global__ void __launch_bounds__(kTabThreads) cache_compact_kernel(const __grid_constant__ CacheCompactArgs a) {
+  using Team = Team<kTabCtas>;
+  __shared__ int row_pages[kMaxSeqs];  // pages of every sequence
   __shared__ int sums[32], sums2[32], live_count[kTabCtas], move_count[kTabCtas];
   const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = Team::rank();
   constexpr int kThreads = kTabCtas * kTabThreads;
   bool bad = false;
   grid_dep_wait();
   grid_dep_launch();
+
+  const int mine_in =
+      tid < a.batch ? pages_of(checked_len(a.lens[tid], a.max_pages, a.page_shift, &bad), a.page_shift) : 0;
+  row_pages[tid] = mine_in;
+  const int longest = block_max(mine_in, sums2);
 
   // live pages, counted in a contiguous run per thread
   const int per_cta = (a.n_pages + kTabCtas - 1) / kTabCtas;
@@ -241,8 +298,8 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
   for (int p = p0; p < p1; ++p) mine += a.refs_in[p] > 0;
   int cta_live = 0;
   block_scan(mine, sums, &cta_live);
-  if (tid == 0) publish(live_count, rank, cta_live);
-  cluster_sync_all();
+  if (tid == 0) Team::publish(live_count, rank, cta_live);
+  Team::sync();
   int n = 0;
 #pragma unroll
   for (int r = 0; r < kTabCtas; ++r) n += live_count[r];
@@ -261,10 +318,10 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
   const int move_end = block_scan(moves, sums, &cta_moves);
   __shared__ int hole_count[kTabCtas];
   if (tid == 0) {
-    publish(hole_count, rank, cta_holes);
-    publish(move_count, rank, cta_moves);
+    Team::publish(hole_count, rank, cta_holes);
+    Team::publish(move_count, rank, cta_moves);
   }
-  cluster_sync_all();
+  Team::sync();
   int hole_at = hole_end - holes, move_at = move_end - moves, total = 0;
 #pragma unroll
   for (int r = 0; r < kTabCtas; ++r) {
@@ -287,7 +344,7 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
     a.counts[0] = n;
     a.counts[1] = total;
   }
-  cluster_sync_all();
+  Team::sync();
 
   for (int i = rank * kTabThreads + tid; i < total; i += kThreads) {
     const int src = __ldcg(a.copy_src + i), dst = __ldcg(a.copy_dst + i);
@@ -296,17 +353,25 @@ __global__ void __cluster_dims__(kTabCtas, 1, 1) __launch_bounds__(kTabThreads)
     a.refs_out[dst] = refs;
     if (a.refs_out == a.refs_in) a.refs_out[src] = 0;
   }
-  cluster_sync_all();
+  Team::sync();
 
-  for (int b = rank * kTabWarps + (tid >> 5); b < a.batch; b += kTabCtas * kTabWarps) {
-    const int used = pages_of(checked_len(a.lens[b], a.max_pages, a.page_shift, &bad), a.page_shift);
-    const int32_t* row = a.table_in + static_cast<int64_t>(b) * a.max_pages;
-    int32_t* dst = a.table_out + static_cast<int64_t>(b) * a.max_pages;
-    for (int j = lane; j < used; j += 32) {
-      const int p = row[j];
-      if (p >= 0 && p < a.n_pages) dst[j] = __ldcg(a.page_map + p);
+  const int pieces = (longest + kPiece - 1) / kPiece;
+  for (int64_t w = rank * kTabWarps + (tid >> 5); w < static_cast<int64_t>(a.batch) * pieces; w += kTabCtas * kTabWarps) {
+    const int b = static_cast<int>(w / pieces), j0 = static_cast<int>(w - static_cast<int64_t>(b) * pieces) * kPiece;
+    const int32_t* row = a.table_in + static_cast<int64_t>(b) * a.max_pages + j0 + lane;
+    int32_t* dst = a.table_out + static_cast<int64_t>(b) * a.max_pages + j0 + lane;
+    int32_t x[kPiece / 32];
+#pragma unroll
+    for (int u = 0; u < kPiece / 32; ++u) {
+      x[u] = -1;
+      if (j0 + lane + 32 * u >= row_pages[b]) continue;
+      const int p = row[32 * u];
+      if (p >= 0 && p < a.n_pages) x[u] = __ldcg(a.page_map + p);
       else bad = true;
     }
+#pragma unroll
+    for (int u = 0; u < kPiece / 32; ++u)
+      if (x[u] >= 0) dst[32 * u] = x[u];
   }
   if (bad) atomicOr(a.status, kDevPageIndex);
 }
@@ -365,8 +430,11 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 // ---- appended rows -----------------------------------------------------------------------------
-// A warp per row: k and v of all heads in 16-byte pieces, then the log-gate.
-__global__ void __launch_bounds__(256) cache_append_kernel(const CacheAppendArgs a) {
+// A warp per row: where it goes, then its k and v of all heads, eight 16-byte pieces a lane in
+// flight.  12700 rows of 8 x 128 bf16 take 20.5 us (floor 16.2; the lookups and the launch are the
+// rest).  A CTA that looks up 64 rows at once and streams them with all threads took 22.0.
+constexpr int kAppendUnroll = 8;
+__global__ void __launch_bounds__(256, 4) cache_append_kernel(const __grid_constant__ CacheAppendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
@@ -393,16 +461,24 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const CacheAppendArgs
       continue;
     }
     const int off = static_cast<int>(pos & (page - 1));
+    const int64_t base = (static_cast<int64_t>(at) * a.hkv * page + off) * hv;
     const uint4* ks = static_cast<const uint4*>(a.k) + r * row_vecs;
     const uint4* vs = static_cast<const uint4*>(a.v) + r * row_vecs;
-    uint4* kd = static_cast<uint4*>(a.k_pages);
-    uint4* vd = static_cast<uint4*>(a.v_pages);
-    for (int i = lane; i < row_vecs; i += 32) {
-      const int head = i / hv, piece = i - head * hv;
-      const int64_t to = ((static_cast<int64_t>(at) * a.hkv + head) * page + off) * hv + piece;
-      const uint4 kx = ks[i], vx = vs[i];
-      kd[to] = kx;
-      vd[to] = vx;
+    for (int i0 = lane; i0 < 2 * row_vecs; i0 += 32 * kAppendUnroll) {
+      uint4 x[kAppendUnroll];
+#pragma unroll
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        const int i = i0 + 32 * u;
+        if (i < 2 * row_vecs) x[u] = i < row_vecs ? ks[i] : vs[i - row_vecs];
+      }
+#pragma unroll
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        const int i = i0 + 32 * u;
+        if (i >= 2 * row_vecs) break;
+        const int j = i < row_vecs ? i : i - row_vecs;
+        const int head = j / hv;
+        static_cast<uint4*>(i < row_vecs ? a.k_pages : a.v_pages)[base + static_cast<int64_t>(head) * page * hv + (j - head * hv)] = x[u];
+      }
     }
     if (lane == 0 && a.logsig_pages)
       a.logsig_pages[static_cast<int64_t>(at) * page + off] = a.logsig ? a.logsig[r] : 0.0f;
@@ -411,13 +487,42 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const CacheAppendArgs
 
 }  // namespace
 
+namespace {
+
+// A table call's launch: one CTA, or a cluster of eight when there is enough to share.
+template <typename Args>
+cudaError_t launch_tables(void (*one)(Args), void (*eight)(Args), bool small, const Args& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(small ? 1 : kMaxTabCtas);
+  cfg.blockDim = dim3(kTabThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kMaxTabCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = small ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, small ? one : eight, a);
+}
+
+// One CTA up to 4096 pages and 64 sequences, the cluster beyond: on the device an update of 32
+// sequences of 64 pages takes 7.9 us in one CTA and 9.1 in the cluster, of 256 sequences of 8 pages
+// 16.7 and 11.4, of one sequence in a pool of 16384 pages 11.0 and 6.7.
+bool small_tables(int n_pages, int batch) { return n_pages <= 4096 && batch <= 64; }
+
+}  // namespace
+
 tg_status launch_cache_update(const CacheUpdateArgs& a, cudaStream_t st) {
-  return cuda_check(launch_pdl(cache_update_kernel, dim3(kTabCtas), dim3(kTabThreads), 0, st, a),
+  return cuda_check(launch_tables(cache_update_kernel<1>, cache_update_kernel<kMaxTabCtas>,
+                                  small_tables(a.n_pages, a.batch_in > a.batch_out ? a.batch_in : a.batch_out), a, st),
                     "cache update launch");
 }
 
 tg_status launch_cache_compact(const CacheCompactArgs& a, cudaStream_t st) {
-  return cuda_check(launch_pdl(cache_compact_kernel, dim3(kTabCtas), dim3(kTabThreads), 0, st, a),
+  return cuda_check(launch_tables(cache_compact_kernel<1>, cache_compact_kernel<kMaxTabCtas>,
+                                  small_tables(a.n_pages, a.batch), a, st),
                     "cache compact launch");
 }
 
@@ -445,7 +550,7 @@ tg_status launch_cache_copy(const tg_page_pool* pools, int n_pools, int n_pages,
 
 tg_status launch_cache_append(const CacheAppendArgs& a, cudaStream_t st) {
   int64_t blocks = (a.rows + 7) / 8;
-  const int64_t cap = static_cast<int64_t>(num_sms()) * 8;
+  const int64_t cap = static_cast<int64_t>(num_sms()) * 4;
   if (blocks > cap) blocks = cap;
   return cuda_check(launch_pdl(cache_append_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a),
                     "cache append launch");
