@@ -15,13 +15,13 @@
 // matter.  A chunk finds its threshold by bisection over the threads' maxima, one
 // barrier with a count per step; it stops as soon as the count is close to n.
 //
-// What bounds them: the chunk kernel its instructions (about 450 a thread for 64
+// What bounds them: the chunk kernel its instructions (about 900 a thread for 64
 // logits; the exponentials alone are 2.8 us of the special-function units for 96
-// rows of 131071) and its barriers, the merge the chain of dependent steps of one
-// CTA per group (log-sums in 64 bits 1.4 us, rankings 3 us).  96 rows of 131071
-// bf16 logits take 18.2 us on the device (HBM floor 3.9), 4 rows of 32000 fp32
-// 7.1 us.  Finding a chunk's threshold by comparing every thread's maximum with
-// every other's took 48 us instead of 10 for the chunks.
+// rows of 131071) and the chain of its barriers, the merge the dependent steps of
+// one CTA per group (log-sums in 64 bits 1.5 us, rankings 1.8 us).  96 rows of
+// 131071 bf16 logits take 16.3 us on the device (HBM floor 3.9), 4 rows of 32000
+// fp32 7.0 us.  With a chunk's threshold found by comparing every thread's maximum
+// with every other's the chunks took 48 us instead of 12.
 //
 // The scores are compared in 64 bits: beams meet at sums that differ in the last
 // places of 32, and a chunk's sum in 32 bits (at most 64 terms per thread, then a tree)
@@ -41,6 +41,7 @@ constexpr int kPerThread = 128 / static_cast<int>(sizeof(T));
 template <typename T>
 constexpr int kChunk = kChunkThreads * kPerThread<T>;
 constexpr int kChunkKeys = 2048;  // room for a chunk's collected keys
+constexpr int kBatch = 8;         // keys a ranking compares at a time (arrays are that much longer than they need be)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kInvLog2e = 1.0 / kLog2e;
 constexpr int kMergeThreads = 512;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kChunkThreads, 4)
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
   constexpr int kWarps = kChunkThreads / 32;
   static_assert(kChunkKeys >= (kMaxOut - 1) * 32, "most logits of a chunk in which fewer than n threads have any");
-  __shared__ __align__(16) uint64_t found[kChunkKeys];
+  __shared__ __align__(16) uint64_t found[kChunkKeys + kBatch];
   __shared__ int n_found;
   __shared__ uint32_t red_max[kWarps], red_min[kWarps];
   __shared__ float red_sum[kWarps];
@@ -225,12 +226,14 @@ __global__ void __launch_bounds__(kChunkThreads, 4)
   const int n = n_found;
   uint64_t* out = ws.keys + (row * chunks + chunk) * n_out;
   if (n <= kChunkKeys) {
-    for (int i = warp; i < n; i += kWarps) {  // a warp per key
+    for (int i = tid; i < n; i += kChunkThreads) {
       const uint64_t k = found[i];
       int above = 0;
-      for (int j = 0; j < n; j += 32)
-        above += __popc(__ballot_sync(0xffffffffu, j + lane < n && found[j + lane] > k));
-      if (lane == 0 && above < n_out) out[above] = k;
+      for (int j = 0; j < n; j += kBatch) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) above += (found[j + u] > k) & (j + u < n);
+      }
+      if (above < n_out) out[above] = k;
     }
     for (int i = n + tid; i < n_out; i += kChunkThreads) out[i] = 0;
   } else {
@@ -292,10 +295,10 @@ __global__ void __launch_bounds__(kMergeThreads)
   extern __shared__ __align__(16) uint8_t smem[];
   const int lists = beams * chunks;
   const int room = n_out * (n_out + 1) / 2;
-  uint64_t* const head_score = reinterpret_cast<uint64_t*>(smem);                // [lists]
-  uint64_t* const found_score = head_score + lists;                              // [room]
-  uint32_t* const head_place = reinterpret_cast<uint32_t*>(found_score + room);  // [lists]
-  uint32_t* const found_place = head_place + lists;                              // [room]
+  uint64_t* const head_score = reinterpret_cast<uint64_t*>(smem);                         // [lists]
+  uint64_t* const found_score = head_score + lists + kBatch;                              // [room]
+  uint32_t* const head_place = reinterpret_cast<uint32_t*>(found_score + room + kBatch);  // [lists]
+  uint32_t* const found_place = head_place + lists + kBatch;                              // [room]
   __shared__ double log_sum[TG_MAX_BEAMS];
   __shared__ int ranked[kMaxOut];  // the lists by their heads
   __shared__ Cand limit;           // the n-th head
@@ -348,17 +351,21 @@ __global__ void __launch_bounds__(kMergeThreads)
     head_place[l] = c.place;
   }
   __syncthreads();
-  // a warp per head: how many heads come before it
-  for (int l = warp; l < lists; l += kWarps) {
+  // how many of n places come before c
+  auto ahead = [](const uint64_t* score, const uint32_t* place, int n, const Cand& c) {
+    int above = 0;
+    for (int j = 0; j < n; j += kBatch) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) above += before(Cand{score[j + u], place[j + u]}, c) & (j + u < n);
+    }
+    return above;
+  };
+  for (int l = tid; l < lists; l += kMergeThreads) {
     const Cand c = {head_score[l], head_place[l]};
     if (!c.score) continue;
-    int above = 0;
-    for (int j = 0; j < lists; j += 32)
-      above += __popc(__ballot_sync(0xffffffffu, j + lane < lists && before(Cand{head_score[j + lane], head_place[j + lane]}, c)));
-    if (lane == 0 && above < n_out) {
-      ranked[above] = l;
-      if (above == n_out - 1) limit = c;
-    }
+    const int above = ahead(head_score, head_place, lists, c);
+    if (above < n_out) ranked[above] = l;
+    if (above == n_out - 1) limit = c;
   }
   __syncthreads();
   // The list whose head is r-th can add n - r candidates: r heads and its own earlier ones come
@@ -377,12 +384,10 @@ __global__ void __launch_bounds__(kMergeThreads)
   __syncthreads();
   const int n = n_found;
   const int64_t out = static_cast<int64_t>(blockIdx.x) * n_out;
-  for (int i = warp; i < n; i += kWarps) {
+  for (int i = tid; i < n; i += kMergeThreads) {
     const Cand c = {found_score[i], found_place[i]};
-    int above = 0;
-    for (int j = 0; j < n; j += 32)
-      above += __popc(__ballot_sync(0xffffffffu, j + lane < n && before(Cand{found_score[j + lane], found_place[j + lane]}, c)));
-    if (lane != 0 || above >= n_out) continue;
+    const int above = ahead(found_score, found_place, n, c);
+    if (above >= n_out) continue;
     const uint32_t beam = c.place / static_cast<uint32_t>(vocab);
     scores_out[out + above] = static_cast<float>(from_order_key64(c.score));
     parent_out[out + above] = static_cast<int32_t>(row0 + beam);
@@ -419,7 +424,7 @@ tg_status launch_beam_select(const void* logits, tg_dtype dt, const float* score
                        static_cast<const float*>(logits), vocab, n_out, chunks, ws);
   if (e != cudaSuccess) return cuda_check(e, "beam chunk launch");
   const size_t per_group = static_cast<size_t>(beams) * chunks;
-  const size_t smem = (per_group + n_out * (n_out + 1) / 2) * (sizeof(uint64_t) + sizeof(uint32_t));
+  const size_t smem = (per_group + n_out * (n_out + 1) / 2 + 2 * kBatch) * (sizeof(uint64_t) + sizeof(uint32_t));
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return cuda_check(e, "beam merge shared memory");
