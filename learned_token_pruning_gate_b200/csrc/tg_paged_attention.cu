@@ -37,8 +37,8 @@
 // of 1151 to 131073 tokens 138 us (99% of the copy rate), 16 of 2304 to 2817 33 us
 // (77%), one of 320 6.8 us.  About 5 us of a call are latency: lengths, table and
 // first rows one after another (2.5 us), the last sums and the join.  32 query
-// heads over 4 of 64, 61 sequences of up to 4353 tokens: 32.6 us (63%); fp32, 4
-// over 2 of 64, 33 sequences of 256 to 1024: 10.0 us (30%).
+// heads over 4 of 64, 61 sequences of up to 4353 tokens: 31.2 us (65%); fp32, 4
+// over 2 of 64, 33 sequences of 256 to 1024: 9.7 us (31%).
 //
 // Maxima move lazily: a warp keeps its reference maximum until a logit exceeds it
 // by more than 8, so that weights stay below e^8 and the accumulators are rarely
@@ -715,12 +715,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(sizeof(T) == 2, Core::kH
   if (bad) atomicOr(p.a.status, kDevPageIndex);
 }
 
-// The parts of one head of a shared unit, joined in order: a warp takes every kWarps-th part, four
-// at a time, a lane D / 32 columns of them; then the warps' sums.
+// The parts of a shared unit, joined in the order of the list.  With few parts the first block of a
+// unit joins all its heads, a warp each; with many every block takes one head, and its warps every
+// kJoinWarps-th part.  (With a block for every head in both cases a call of 61 sequences with 8 heads
+// to a kv head took 32.6 us for 31.2.)
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kFewParts = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Plan p, int heads) {
-  constexpr int kJoinWarps = kJoinThreads / 32;
   constexpr int kPer = D / 32;
   __shared__ float part_m[kJoinWarps], part_l[kJoinWarps], part_o[kJoinWarps][D];
   grid_dep_wait();
@@ -728,37 +731,62 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t unit = blockIdx.x;
   const int2 share = p.shares[unit];
-  if (share.y < share.x) return;
+  const bool few = share.y - share.x < kFewParts;
+  if (share.y < share.x || (few && blockIdx.y > 0)) return;
   const int b = static_cast<int>(unit / p.units), u = static_cast<int>(unit - static_cast<int64_t>(b) * p.units);
-  const int hk = u / p.blocks, block = u - hk * p.blocks, h = blockIdx.y;
-  if (h >= p.group - block * heads) return;
+  const int hk = u / p.blocks, block = u - hk * p.blocks;
+  const int nh = min(heads, p.group - block * heads), h0 = hk * p.group + block * heads;
   const int64_t slot = slot_floats(heads, D);
-  float m = -INFINITY, l = 0.0f, o[kPer] = {};
-  for (int c = share.x + warp; c <= share.y; c += 4 * kJoinWarps) {
-    float pm[4], pl[4], po[4][kPer];
+
+  // head h of every `step`-th part from `first` on, four parts at a time; a lane has D / 32 columns
+  float m, l, o[kPer];
+  auto join = [&](int h, int first, int step) {
+    m = -INFINITY;
+    l = 0.0f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int cc = c + x * kJoinWarps;
-      const float* part = p.partial + (2 * cc + (cc == share.x)) * slot;
-      pm[x] = cc <= share.y ? part[heads * D + h] : -INFINITY;
-      pl[x] = cc <= share.y ? part[heads * D + heads + h] : 0.0f;
+    for (int e = 0; e < kPer; ++e) o[e] = 0.0f;
+    for (int c = first; c <= share.y; c += 4 * step) {
+      float pm[4], pl[4], po[4][kPer];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) po[x][e] = cc <= share.y ? part[h * D + lane + 32 * e] : 0.0f;
+      for (int x = 0; x < 4; ++x) {
+        const int cc = c + x * step;
+        const float* part = p.partial + (2 * cc + (cc == share.x)) * slot;
+        pm[x] = cc <= share.y ? part[heads * D + h] : -INFINITY;
+        pl[x] = cc <= share.y ? part[heads * D + heads + h] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) po[x][e] = cc <= share.y ? part[h * D + lane + 32 * e] : 0.0f;
+      }
+      const float top = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
+      const float c_old = weight(m, top);
+      m = top;
+      l *= c_old;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] *= c_old;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float w = weight(pm[x], top);
+        l = fmaf(pl[x], w, l);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = fmaf(po[x][e], w, o[e]);
+      }
     }
-    const float top = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
-    const float c_old = weight(m, top);
-    m = top;
-    l *= c_old;
+  };
+  auto out = [&](int h, int d, float x, float top, float sum) {
+    put(static_cast<T*>(p.a.out) + (static_cast<int64_t>(b) * p.a.hq + h0 + h) * D + d, sum == 0.0f ? 0.0f : x / sum);
+    if (d == 0 && p.a.lse)
+      p.a.lse[static_cast<int64_t>(h0 + h) * p.a.batch + b] = sum == 0.0f ? -INFINITY : top + logf(sum);
+  };
+  if (few) {
+    for (int h = warp; h < nh; h += kJoinWarps) {
+      join(h, share.x, 1);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] *= c_old;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float w = weight(pm[x], top);
-      l = fmaf(pl[x], w, l);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = fmaf(po[x][e], w, o[e]);
+      for (int e = 0; e < kPer; ++e) out(h, lane + 32 * e, o[e], m, l);
     }
+    return;
   }
+  const int h = blockIdx.y;
+  if (h >= nh) return;
+  join(h, share.x + warp, kJoinWarps);
   if (lane == 0) {
     part_m[warp] = m;
     part_l[warp] = l;
@@ -777,10 +805,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     sum = fmaf(part_l[w], c, sum);
     x = fmaf(part_o[w][d], c, x);
   }
-  const int head = hk * p.group + block * heads + h;
-  put(static_cast<T*>(p.a.out) + (static_cast<int64_t>(b) * p.a.hq + head) * D + d, sum == 0.0f ? 0.0f : x / sum);
-  if (d == 0 && p.a.lse)
-    p.a.lse[static_cast<int64_t>(head) * p.a.batch + b] = sum == 0.0f ? -INFINITY : top + logf(sum);
+  out(h, d, x, top, sum);
 }
 
 template <typename T, int D, typename Core>
