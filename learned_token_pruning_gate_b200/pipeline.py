@@ -212,9 +212,10 @@ class PagedCache:
 
     k, v: [layers, pages, Hkv, page_size, d]; logsig: [pages, page_size] fp32, one for all
     layers.  grow() makes room for new tokens (and forks or frees sequences), append() writes a
-    layer's rows there, attend() reads them; nothing of it waits for the GPU or allocates.  A
-    captured graph may hold any of these calls; the tables of a fork alternate between two
-    buffers, so capture forks in pairs.
+    layer's rows there, attend() reads them; nothing of it waits for the GPU.  The calls of one
+    cache belong on one stream, in order.  A captured graph may hold any of them; the tables of a
+    fork alternate between two buffers, so capture forks in pairs, and call attend() once before
+    (its first call for a number of query heads allocates the workspace that they share).
 
     After grow(), start [batch] holds the position of each sequence's first new token, -1 where it
     did not fit (its rows are then skipped by append())."""
