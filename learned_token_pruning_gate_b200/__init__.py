@@ -716,7 +716,7 @@ def _addr(t):
 
 def _on(index):
     """Makes CUDA device `index` current for a call; nothing to do when it is already."""
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:  # (a tensor lives there: CUDA is initialised)
         return _SAME_DEVICE
     return torch.cuda.device(index)
 
@@ -729,10 +729,10 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _workspace(workspace, device):
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or \
-            workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+def _workspace(workspace, index):
+    if not (workspace.dtype is torch.uint8 and workspace.get_device() == index
+            and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
 
 
 def _expect_pools(k_pages, v_pages, logsig_pages):
@@ -803,7 +803,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=No
     P, Hkv, page, d = pool = k_pages.shape
     max_pages = table.shape[1]
     if workspace is not None and not isinstance(workspace, str):
-        _workspace(workspace, q.device)
+        _workspace(workspace, i)
     if not (i >= 0 and d == dh and Hkv > 0 and Hq % Hkv == 0 and q.is_contiguous()
             and _fits(k_pages, pool, dt, i) and _fits(v_pages, pool, dt, i)
             and _fits(table, (B, max_pages), i32, i) and _fits(lens, (B,), i32, i)
@@ -820,7 +820,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=No
         temp = one if temp is None else temp
         out = torch.empty_like(q) if out is None else out
         if want_lse and lse is None:
-            lse = torch.empty((Hq, B), dtype=f32, device=q.device)
+            lse = q.new_empty((Hq, B), dtype=f32)
         if isinstance(workspace, str):
             workspace = paged_attention_workspace(B, Hq, Hkv, dh, dt, q.device)
         # a workspace of no bytes has no address: the call needs none of it
@@ -879,10 +879,10 @@ def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_o
                              start, copy_src, copy_dst)
     with _on(i):
         if table_out is None:
-            table_out = torch.full((Bo, mp), -1, dtype=i32, device=table.device)
+            table_out = table.new_full((Bo, mp), -1)
         refs_out = torch.empty_like(refs) if refs_out is None else refs_out
         if len(given) < 4:  # one allocation for those that are not given
-            fresh = torch.empty((4, Bo), dtype=i32, device=table.device).unbind()
+            fresh = table.new_empty((4, Bo)).unbind()
             small = fresh if not given else [f if t is None else t for f, t in zip(fresh, small)]
         lens_out, start, copy_src, copy_dst = small
         _check("tg_cache_update", library().tg_cache_update(
@@ -918,10 +918,10 @@ def cache_compact(table, lens, refs, page_size, table_out=None, refs_out=None):
         _expect_cache_compact(table, lens, refs, table_out, refs_out)
     with _on(i):
         if table_out is None:
-            table_out = torch.full(shape, -1, dtype=i32, device=table.device)
+            table_out = table.new_full(shape, -1)
         refs_out = torch.empty_like(refs) if refs_out is None else refs_out
-        page_map, src, dst = torch.empty((3, P), dtype=i32, device=table.device).unbind()
-        counts = torch.empty(2, dtype=i32, device=table.device)
+        page_map, src, dst = table.new_empty((3, P)).unbind()
+        counts = table.new_empty(2)
         _check("tg_cache_compact", library().tg_cache_compact(
             table.data_ptr(), lens.data_ptr(), shape[0], refs.data_ptr(), P, page_size, shape[1],
             table_out.data_ptr(), refs_out.data_ptr(), page_map.data_ptr(), src.data_ptr(),
@@ -1041,7 +1041,7 @@ def gated_delta_step(q, k, v, log_alpha, beta, state, parent=None, eps=1e-6, out
     with _on(i):
         out = torch.empty_like(q) if out is None else out
         if state_out is None:
-            state_out = torch.empty((B, H, d, d), dtype=f32, device=q.device)
+            state_out = q.new_empty((B, H, d, d), dtype=f32)
         _check("tg_gated_delta_step", library().tg_gated_delta_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), log_alpha.data_ptr(),
             beta.data_ptr(), B, H, d, eps, state.data_ptr(), S,
@@ -1070,7 +1070,7 @@ def beam_select(logits, scores, n_out=None, workspace=None):
     V = logits.shape[1]
     i, dev = logits.get_device(), logits.device
     if workspace is not None:
-        _workspace(workspace, dev)
+        _workspace(workspace, i)
     if not (i >= 0 and _fits(logits, (G * beams, V), logits.dtype, i)
             and _fits(scores, (G, beams), torch.float32, i)):
         _expect("logits", logits, (G * beams, V), logits.dtype, dev)
@@ -1080,7 +1080,7 @@ def beam_select(logits, scores, n_out=None, workspace=None):
     with _on(i):
         if workspace is None:
             workspace = beam_select_workspace(G, beams, V, n_out, dev)
-        best, parent, token = torch.empty((3, G, n_out), dtype=torch.int32, device=dev).unbind()
+        best, parent, token = scores.new_empty((3, G, n_out), dtype=torch.int32).unbind()
         best = best.view(torch.float32)
         _check("tg_beam_select", library().tg_beam_select(
             logits.data_ptr(), _dtype_code(logits), scores.data_ptr(), G, beams, V, n_out,
