@@ -390,11 +390,13 @@ struct CoreFp32 {
     for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float x = 0.0f;
+        float2 a = make_float2(0.0f, 0.0f), b = a;
 #pragma unroll
-        for (int c = 0; c < kVec; ++c)
-          x = fmaf(q[h][c].x, k[r][c].x,
-                   fmaf(q[h][c].y, k[r][c].y, fmaf(q[h][c].z, k[r][c].z, fmaf(q[h][c].w, k[r][c].w, x))));
+        for (int c = 0; c < kVec; ++c) {
+          a = __ffma2_rn(make_float2(q[h][c].x, q[h][c].y), make_float2(k[r][c].x, k[r][c].y), a);
+          b = __ffma2_rn(make_float2(q[h][c].z, q[h][c].w), make_float2(k[r][c].z, k[r][c].w), b);
+        }
+        float x = (a.x + a.y) + (b.x + b.y);
 #pragma unroll
         for (int w = 1; w < 8; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
         s[h][r] = gate[r] == -INFINITY ? -INFINITY : fmaf(x, scale[h], gain[h] * gate[r]);
@@ -428,10 +430,9 @@ struct CoreFp32 {
         l[h] += w;
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-          o[h][c].x = fmaf(w, v[r][c].x, o[h][c].x);
-          o[h][c].y = fmaf(w, v[r][c].y, o[h][c].y);
-          o[h][c].z = fmaf(w, v[r][c].z, o[h][c].z);
-          o[h][c].w = fmaf(w, v[r][c].w, o[h][c].w);
+          const float2 a = __ffma2_rn(make_float2(w, w), make_float2(v[r][c].x, v[r][c].y), make_float2(o[h][c].x, o[h][c].y));
+          const float2 b = __ffma2_rn(make_float2(w, w), make_float2(v[r][c].z, v[r][c].w), make_float2(o[h][c].z, o[h][c].w));
+          o[h][c] = make_float4(a.x, a.y, b.x, b.y);
         }
       }
   }

@@ -238,6 +238,33 @@ def test_attention_on_two_streams():
         assert all(torch.equal(x, want) for x in o)
 
 
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different shapes on one workspace, replayed in turn with eager calls between."""
+    ps = [gen.paged_inputs(lens, 16, 8, 128, 64, 30 + i) for i, lens in enumerate(([1500, 700], [64, 2500, 9]))]
+    ds = [{n: dev(t) for n, t in p.items()} for p in ps]
+    ws = tg.paged_attention_workspace(3, 16, 8, 128)
+    outs = [torch.empty_like(d["q"]) for d in ds]
+
+    def call(i):
+        d = ds[i]
+        tg.paged_attention(d["q"], d["k_pages"], d["v_pages"], d["table"], d["lens"], d["logsig_pages"], d["gain"],
+                           d["temp"], out=outs[i], workspace=ws)
+    want, graphs = [], []
+    for i in range(2):
+        call(i)
+        want.append(outs[i].clone())
+        _check_attention(ps[i], *_attend(ps[i]))
+        graphs.append(torch.cuda.CUDAGraph())
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graphs[i]):
+            call(i)
+    for i in (0, 1, 1, 0, 1):
+        outs[i].zero_()
+        call(1 - i)
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i]) and torch.equal(outs[1 - i], want[1 - i])
+
+
 def test_attention_far_pages():
     """Offsets past 2^31 elements and 2^32 bytes: the last pages of a pool of 5 GB."""
     P, Hkv, page, d = 9000, 8, 128, 128
