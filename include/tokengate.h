@@ -563,9 +563,9 @@ TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int3
  *   lse   device [n_q_heads, batch] fp32 or NULL
  *   workspace, workspace_bytes
  *         device scratch of tg_paged_attention_workspace_bytes, or NULL.  With it
- *         the keys of a sequence are split over several SMs and joined in a fixed
- *         order; without it one SM reads them all.  16-byte aligned, any
- *         contents.  TG_ERR_WORKSPACE when smaller.  Calls that share a workspace
+ *         the keys of a sequence are split over all SMs and joined in a fixed
+ *         order; without it one SM reads them (a few when the tables are few and
+ *         short).  16-byte aligned, any contents.  TG_ERR_WORKSPACE when smaller.  Calls that share a workspace
  *         must not overlap on the GPU.
  *   head_dim 64 or 128, n_q_heads <= 512, batch * max_pages * page_size <= 2^36;
  *   q, k_pages, v_pages and out 16-byte aligned.

@@ -48,6 +48,13 @@ def _attend(p, workspace="auto", **kw):
                               want_lse=True, workspace=workspace, **kw)
 
 
+def _wide(p, entries=8192):
+    """The same cache with room for more pages in the table: the kernel is chosen by what a table can hold."""
+    t = torch.full((p["table"].shape[0], entries), -1, dtype=torch.int32)
+    t[:, :p["table"].shape[1]] = p["table"]
+    return dict(p, table=t)
+
+
 def _check_attention(p, got, lse, what=""):
     h = {n: host_f32(t) if t.is_floating_point() else t.numpy() for n, t in p.items()}
     ref, rlse, mag = do.paged_attention(h["q"], h["k_pages"], h["v_pages"], h["table"], h["lens"],
@@ -81,8 +88,22 @@ def _check_attention(p, got, lse, what=""):
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attention_matches_oracle(lens, Hq, Hkv, d, page, dtype):
     p = gen.paged_inputs(lens, Hq, Hkv, d, page, 3, dtype)
-    _check_attention(p, *_attend(p), "split")
-    _check_attention(p, *_attend(p, workspace=None), "one SM")
+    _check_attention(p, *_attend(p), "as it is")
+    _check_attention(p, *_attend(p, workspace=None), "without a workspace")
+    _check_attention(p, *_attend(_wide(p)), "wide table")
+    _check_attention(p, *_attend(_wide(p), workspace=None), "wide table, one SM")
+
+
+@pytest.mark.parametrize("entries", [1, 2, 3, 5, 8, 9, 31, 32, 33, 100])
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("bf16", 4, 2, 128), ("bf16", 24, 1, 64), ("fp32", 8, 2, 64)])
+def test_attention_every_cluster_size(entries, dtype, Hq, Hkv, d):
+    """Tables of 64 to 6400 tokens: a unit on one CTA, on clusters of two to eight, and on the list."""
+    full = entries * 64
+    lens = sorted({full, full - 1, max(full - 65, 0), full // 2, 1, 0})
+    p = gen.paged_inputs(lens, Hq, Hkv, d, 64, entries, dtype, max_pages=entries)
+    _check_attention(p, *_attend(p), "few")
+    many = gen.paged_inputs([full] + [1] * 40, Hq, Hkv, d, 64, entries, dtype, max_pages=entries)
+    _check_attention(many, *_attend(many), "many")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -107,7 +128,8 @@ def test_attention_masked_tokens(dtype):
     h = {n: host_f32(x) if x.is_floating_point() else x.numpy() for n, x in p.items()}
     assert not host_f32(out)[1].any()
     _check_attention(p, out, lse, "masked")
-    _check_attention(p, *_attend(p, workspace=None), "masked, one SM")
+    _check_attention(p, *_attend(p, workspace=None), "masked, without a workspace")
+    _check_attention(p, *_attend(_wide(p)), "masked, wide table")
     assert h["gain"][0] == 0.0
 
 
@@ -127,9 +149,10 @@ def test_attention_all_gates_lowest(dtype):
     assert np.isfinite(lse.cpu().numpy()).all()
 
 
-def test_attention_defaults_and_workspace_reuse():
+@pytest.mark.parametrize("widen", [lambda p: p, _wide])
+def test_attention_defaults_and_workspace_reuse(widen):
     """No gates, gains or temperatures; one workspace over calls of different lengths and shapes."""
-    p = gen.paged_inputs([900, 20, 0, 411], 16, 8, 128, 64, 7)
+    p = widen(gen.paged_inputs([900, 20, 0, 411], 16, 8, 128, 64, 7))
     h = {n: host_f32(t) if t.is_floating_point() else t.numpy() for n, t in p.items()}
     ref, _, mag = do.paged_attention(h["q"], h["k_pages"], h["v_pages"], h["table"], h["lens"])
     d = {n: dev(t) for n, t in p.items()}
@@ -175,9 +198,10 @@ def test_attention_bad_table_and_lengths():
     assert torch.equal(out, _attend(whole)[0])
 
 
-def test_attention_repeats_and_replays():
+@pytest.mark.parametrize("widen,longest", [(lambda p: p, 3000), (_wide, 3000), (lambda p: p, 900)])
+def test_attention_repeats_and_replays(widen, longest):
     """The same bits every time, eagerly, from another stream and from a captured graph."""
-    p = gen.paged_inputs([3000, 1, 777, 0, 64], 16, 8, 128, 64, 9)
+    p = widen(gen.paged_inputs([longest, 1, 777, 0, 64], 16, 8, 128, 64, 9))
     d = {n: dev(t) for n, t in p.items()}
     ws = tg.paged_attention_workspace(5, 16, 8, 128)
     out, lse = torch.empty_like(d["q"]), torch.empty((16, 5), device="cuda")
@@ -219,7 +243,7 @@ def test_attention_repeats_and_replays():
 
 def test_attention_on_two_streams():
     """Two calls at once, each with its own workspace, beside a third one's kernels."""
-    ps = [gen.paged_inputs(lens, 16, 8, 128, 64, 20 + i) for i, lens in enumerate(([2000, 33, 900], [5, 3000]))]
+    ps = [_wide(gen.paged_inputs(lens, 16, 8, 128, 64, 20 + i)) for i, lens in enumerate(([2000, 33, 900], [5, 3000]))]
     ds = [{n: dev(t) for n, t in p.items()} for p in ps]
     wss = [tg.paged_attention_workspace(len(p["lens"]), 16, 8, 128) for p in ps]
     outs = [[torch.empty_like(d["q"]) for _ in range(20)] for d in ds]
@@ -240,7 +264,7 @@ def test_attention_on_two_streams():
 
 def test_two_graphs_share_a_workspace():
     """Two captured calls of different shapes on one workspace, replayed in turn with eager calls between."""
-    ps = [gen.paged_inputs(lens, 16, 8, 128, 64, 30 + i) for i, lens in enumerate(([1500, 700], [64, 2500, 9]))]
+    ps = [_wide(gen.paged_inputs(lens, 16, 8, 128, 64, 30 + i)) for i, lens in enumerate(([1500, 700], [64, 2500, 9]))]
     ds = [{n: dev(t) for n, t in p.items()} for p in ps]
     ws = tg.paged_attention_workspace(3, 16, 8, 128)
     outs = [torch.empty_like(d["q"]) for d in ds]
