@@ -21,7 +21,9 @@
 // one CTA per group (log-sums in 64 bits 1.5 us, rankings 1.8 us).  96 rows of
 // 131071 bf16 logits take 16.3 us on the device (HBM floor 3.9), 4 rows of 32000
 // fp32 7.0 us.  With a chunk's threshold found by comparing every thread's maximum
-// with every other's the chunks took 48 us instead of 12.
+// with every other's the chunks took 48 us instead of 12; with a group joined in
+// the CTA that finishes its last chunk, in place of a second launch, the calls
+// took 18.9 and 8.3 us.
 //
 // The scores are compared in 64 bits: beams meet at sums that differ in the last
 // places of 32, and a chunk's sum in 32 bits (at most 64 terms per thread, then a tree)

@@ -599,6 +599,30 @@ def test_beam_select_ties_and_missing(dtype):
     assert tg.beam_select(dev(x), dev(scores), 2)[1].tolist() == [[-1, -1]]
 
 
+def test_beam_select_one_workspace():
+    """One workspace over calls of different shapes and types, eager and replayed: always the same result."""
+    shapes = [(1, 4, 32000, 8, torch.float32), (300, 1, 40, 3, torch.bfloat16), (5, 8, 50001, 16, torch.bfloat16),
+              (2, 3, 7, 4, torch.float32)]
+    g = torch.Generator().manual_seed(5)
+    ws = tg.beam_select_workspace(5, 8, 50001, 16)
+    calls = []
+    for G, beams, V, n, t in shapes:
+        x, s = (2.0 * torch.randn((G * beams, V), generator=g)).to(t), -torch.rand((G, beams), generator=g)
+        calls.append((x, s, n, dev(x), dev(s), tg.beam_select(dev(x), dev(s), n)))
+        _check_beams(x, s, n, calls[-1][5])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = [tg.beam_select(x, s, n, workspace=ws) for _, _, n, x, s, _ in calls]
+    for i in (0, 2, 1, 3, 3, 2, 0):
+        _, _, n, x, s, want = calls[i]
+        got = tg.beam_select(x, s, n, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        graph.replay()
+        for got, (_, _, _, _, _, want) in zip(captured, calls):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_beam_select_largest():
     """The largest sizes: 32 beams of 2^20 logits, 64 candidates; and many groups of one beam."""
     g = torch.Generator("cuda").manual_seed(3)
