@@ -316,7 +316,9 @@ class GatedDecoder:
         lens[:, 0] = np.diff(stack.ck)
         cu = np.concatenate([[0], np.cumsum(lens.reshape(-1))])
         self.cu_prefill = torch.from_numpy(cu.astype(np.int32)).to(dev)
-        self.pos = torch.from_numpy(np.repeat(np.diff(stack.cu), beams).astype(np.int32)).to(dev)
+        self._prompt_ends = torch.from_numpy(np.repeat(np.diff(stack.cu), beams).astype(np.int32)).to(dev)
+        self.pos = self._prompt_ends.clone()
+        self._nobody = torch.full((self.batch,), -1, **i32)
         self._every = np.array([0, np.iinfo(np.int32).max], np.int32)  # positions, as one prompt's rows
         self._rows = np.array([0, self.batch], np.int32)
         self.q = torch.empty((self.batch, stack.Hq, stack.dh), dtype=dt, device=dev)
@@ -325,9 +327,11 @@ class GatedDecoder:
         self.o = torch.empty_like(self.q)
 
     def prefill(self, x):
-        """x [M, d_model] kept rows (overwritten with the stack's output, which is returned)."""
+        """x [M, d_model] kept rows (overwritten with the stack's output, which is returned).  What
+        the cache held before is freed."""
         x, cache_k, cache_v = self.stack.run(x)
-        self.cache.grow(self.cu_prefill)
+        self.cache.grow(self.cu_prefill, parent=self._nobody)
+        self.pos.copy_(self._prompt_ends)
         for i in range(len(self.stack.layers)):
             self.cache.append(i, cache_k[i], cache_v[i], self.stack.logsig)
         return x
