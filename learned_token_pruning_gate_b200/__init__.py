@@ -820,7 +820,7 @@ def paged_attention(q, k_pages, v_pages, table, lens, logsig_pages=None, gain=No
         temp = one if temp is None else temp
         out = torch.empty_like(q) if out is None else out
         if want_lse and lse is None:
-            lse = q.new_empty((Hq, B), dtype=f32)
+            lse = gain.new_empty((Hq, B))
         if isinstance(workspace, str):
             workspace = paged_attention_workspace(B, Hq, Hkv, dh, dt, q.device)
         # a workspace of no bytes has no address: the call needs none of it
@@ -1041,7 +1041,7 @@ def gated_delta_step(q, k, v, log_alpha, beta, state, parent=None, eps=1e-6, out
     with _on(i):
         out = torch.empty_like(q) if out is None else out
         if state_out is None:
-            state_out = q.new_empty((B, H, d, d), dtype=f32)
+            state_out = beta.new_empty((B, H, d, d))
         _check("tg_gated_delta_step", library().tg_gated_delta_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q), log_alpha.data_ptr(),
             beta.data_ptr(), B, H, d, eps, state.data_ptr(), S,
