@@ -299,7 +299,7 @@ class GatedDecoder:
     step(x, parent) runs one new token per sequence: x [batch, d_model], the residuals at the
     gated layers' input.  New tokens take the positions behind their whole prompt (pruned tokens
     included) and have no gate bias.  With `parent` [batch] int32 the sequences are first forked
-    from one another, as beam_select names the parents of a search's beams.
+    from one another: what beam_select returns, flattened.
 
     beams: sequences per prompt.  Sequence p * beams of prompt p gets the prefill; the first step
     forks it (parent = p * beams for all of the prompt's beams)."""
@@ -339,10 +339,14 @@ class GatedDecoder:
     def step(self, x, parent=None):
         """x [batch, d_model] (overwritten with the output, which is returned)."""
         st = self.stack
+        ly = st.layers[0]["wqkv"]
+        if tuple(x.shape) != (self.batch, ly.shape[1]) or x.dtype != ly.dtype:
+            raise ValueError(f"x: {tuple(x.shape)} {x.dtype}, expected "
+                             f"{(self.batch, ly.shape[1])} {ly.dtype}")
+        self.cache.grow(parent=parent)
         if parent is not None:
             # (a freed sequence, parent -1, starts again at position 0)
             self.pos.copy_(torch.where(parent >= 0, self.pos[parent.clamp(min=0).long()], 0))
-        self.cache.grow(parent=parent)
         for i, ly in enumerate(st.layers):
             a = rmsnorm(x, ly["w_ln1"], st.eps)
             qkv = torch.mm(a, ly["wqkv"].t())

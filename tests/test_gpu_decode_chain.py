@@ -66,6 +66,12 @@ def test_steps_continue_the_stack(lens, new, n_layers, dm, Hq, Hkv, dh, inter, d
             ref = want[b][t]
             assert_close(f"prompt {b} token {t}", got[b], ref, tol * np.sqrt(np.mean(ref ** 2)), tol)
     assert d.cache.lens.tolist() == [n + new for n in lens]
+    pos, held = d.pos.clone(), d.cache.lens.clone()
+    for x, parent in ((dev(fresh[0])[:, :-1].contiguous(), None), (dev(fresh[0]).double(), None),
+                      (dev(fresh[0]), torch.zeros(len(lens), dtype=torch.int64, device="cuda"))):
+        with pytest.raises(ValueError):  # refused before anything moves on
+            d.step(x, parent)
+    assert torch.equal(d.pos, pos) and torch.equal(d.cache.lens, held)
 
 
 def test_forked_steps_and_replay():
