@@ -694,7 +694,8 @@ TG_API tg_status tg_gated_delta_step(const void* q, const void* k, const void* v
  * computed in 64 bits from the logits' exponentials summed in 32; larger first,
  * equal ones by lower b * vocab + t.  Only finite scores are candidates: a token
  * of logit -inf, a beam of score -inf, and a beam whose logits hold NaN or +inf
- * offer none.
+ * offer none.  Logits at the lowest value of their type, as masks have it, are
+ * logits like others; a score below what fp32 holds is written as -inf.
  *   logits  device [n_groups * beams, vocab], 16-byte aligned;  scores [n_groups, beams] fp32
  *   scores_out [n_groups, n_out] fp32 in order, parent_out int32 the row r (the
  *   parent of tg_cache_update and tg_gated_delta_step), token_out int32; places

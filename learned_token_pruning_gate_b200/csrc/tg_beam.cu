@@ -26,8 +26,11 @@
 // took 18.9 and 8.3 us.
 //
 // The scores are compared in 64 bits: beams meet at sums that differ in the last
-// places of 32, and a chunk's sum in 32 bits (at most 64 terms per thread, then a tree)
-// is off by less than 1e-7 of itself.
+// places of 32.  A chunk's sum is taken in 32 bits: a term d below the maximum is
+// off by 2^-22 (the approximate exponential) and 2.5 d 2^-24 (difference, product and
+// log2e rounded) of itself, where d averages to at most the log of the chunk's length,
+// 9.7; the additions, 32 and a tree of 14, by 2^-24 each: at most 5e-6 of the sum.  On
+// random logits it is off by some 1e-8.
 #include <cmath>
 
 #include "tg_internal.cuh"
@@ -45,11 +48,10 @@ constexpr int kChunk = kChunkThreads * kPerThread<T>;
 constexpr int kChunkKeys = 2048;  // room for a chunk's collected keys
 constexpr int kBatch = 8;         // keys a ranking compares at a time (arrays are that much longer than they need be)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kInvLog2e = 1.0 / kLog2e;
 constexpr int kMergeThreads = 512;
 
-// What a chunk leaves: per (row, chunk) n keys, and {c, sum 2^(x log2e - c)}, with c the
-// rounded maximum times log2e as fp32 has it (-inf: no finite logit).
+// What a chunk leaves: per (row, chunk) n keys, and {m, sum e^(x - m)}, with m the
+// largest logit (-inf: none above it, and the sum is 0).
 struct BeamWork {
   float2* sums;
   uint64_t* keys;
@@ -177,17 +179,17 @@ __global__ void __launch_bounds__(kChunkThreads, 4)
   __syncthreads();
   const uint32_t top = __reduce_max_sync(0xffffffffu, red_max[lane % kWarps]);
   const uint32_t low = __reduce_min_sync(0xffffffffu, red_min[lane % kWarps]);
-  // Sum of exponentials, 2^(x log2e - c) with one rounding each: c is a number the merge knows
-  // exactly, so rounding the maximum does not shift the sum.  NaN and +inf make it NaN; a chunk
-  // without a logit above -inf leaves 0.
+  // Sum of exponentials, 2^((x - m) log2e).  The maximum is subtracted first: x log2e - m log2e is
+  // off by m's rounding error, in the exponent, and overflows where a mask's value (the lowest of
+  // its type, say) is all that a chunk holds.  NaN and +inf make the sum NaN; a chunk without a
+  // logit above -inf leaves 0.
   const float largest = top >= kLowestKey ? from_order_key(top) : -INFINITY;
-  const float c = largest * kLog2e;
-  const float minus_c = largest == -INFINITY ? 0.0f : -c;
+  const float minus_m = largest == -INFINITY ? 0.0f : -largest;
   float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int e = 0; e < L::kN; e += 2) {
-    const float2 y = __ffma2_rn(make_float2(x.get(e), x.get(e + 1)), make_float2(kLog2e, kLog2e),
-                                make_float2(minus_c, minus_c));
+    const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x.get(e), x.get(e + 1)), make_float2(minus_m, minus_m)),
+                                make_float2(kLog2e, kLog2e));
     s2 = __fadd2_rn(s2, make_float2(exp2_approx(y.x), exp2_approx(y.y)));
   }
   float s = s2.x + s2.y;
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kChunkThreads, 4)
     float total = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) total += red_sum[w];
-    ws.sums[row * chunks + chunk] = make_float2(c, total);
+    ws.sums[row * chunks + chunk] = make_float2(largest, total);
   }
 }
 
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   uint64_t* const found_score = head_score + lists + kBatch;                              // [room]
   uint32_t* const head_place = reinterpret_cast<uint32_t*>(found_score + room + kBatch);  // [lists]
   uint32_t* const found_place = head_place + lists + kBatch;                              // [room]
-  __shared__ double log_sum[TG_MAX_BEAMS];
+  __shared__ double largest[TG_MAX_BEAMS], log_sum[TG_MAX_BEAMS];  // of a beam's logits, and of their e^(x - largest)
   __shared__ int ranked[kMaxOut];  // the lists by their heads
   __shared__ Cand limit;           // the n-th head
   __shared__ int n_found;
@@ -329,12 +331,14 @@ __global__ void __launch_bounds__(kMergeThreads)
     double s = 0.0;
     for (int c = lane; c < chunks; c += 32) {
       const float2 p = part[c];
-      // (the chunks' c are multiples of log2e as fp32 has it)
-      if (p.y != 0.0f) s += static_cast<double>(p.y) * exp((static_cast<double>(p.x) - top) * kInvLog2e);  // NaN stays NaN
+      if (p.y != 0.0f) s += static_cast<double>(p.y) * exp(static_cast<double>(p.x) - top);  // NaN stays NaN
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) log_sum[beam] = static_cast<double>(top) * kInvLog2e + log(s);
+    if (lane == 0) {
+      largest[beam] = top;
+      log_sum[beam] = log(s);
+    }
   }
   __syncthreads();
   auto cand = [&](int list, uint64_t key) {
@@ -342,7 +346,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     Cand c = {0, 0};
     if (key) {
       const uint32_t token = 0xFFFFFFFFu - static_cast<uint32_t>(key);
-      c.score = order_key64(static_cast<double>(scores[row0 + beam]) + (static_cast<double>(logit_of(key)) - log_sum[beam]));
+      // (in this order: log_sum is below the last place of a logit of the type's lowest value)
+      c.score = order_key64(static_cast<double>(scores[row0 + beam]) + ((static_cast<double>(logit_of(key)) - largest[beam]) - log_sum[beam]));
       c.place = static_cast<uint32_t>(beam) * static_cast<uint32_t>(vocab) + token;
     }
     return c;

@@ -161,7 +161,8 @@ def beam_select(logits, scores, n_out):
             x = logits[g * beams + b]
             if np.isnan(x).any() or (x == np.inf).any() or (x == -np.inf).all():
                 continue
-            total = scores[g, b] + (x - (x.max() + np.log(np.exp(x - x.max()).sum())))
+            # (the maximum first: the log of the sum is below the last place of, say, -3e38)
+            total = scores[g, b] + ((x - x.max()) - np.log(np.exp(x - x.max()).sum()))
             order = np.lexsort((np.arange(V), -total))[:n_out]
             found += [(-total[t], b, int(t)) for t in order if np.isfinite(total[t])]
         for i, (s, b, t) in enumerate(sorted(found)[:n_out]):

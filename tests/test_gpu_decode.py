@@ -651,3 +651,42 @@ def test_beam_select_sorted_rows():
     spikes = torch.zeros((1, V))
     spikes[0, 256 * 4:256 * 4 + 64] = torch.arange(64).float() + 1
     _check_beams(spikes, torch.zeros((1, 1)), 64, tg.beam_select(dev(spikes), torch.zeros((1, 1), device="cuda"), 64))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("mask", ["lowest", -1e10, -1e30])
+def test_beam_select_masked_chunks(dtype, mask):
+    """A mask of finite values over whole chunks (16384 logits in bf16, 8192 in fp32), the last, ragged one
+    among them, over all but a few tokens, and over a whole row, whose tokens are then all alike."""
+    t = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    low = torch.finfo(t).min if mask == "lowest" else mask
+    V, beams = 40003, 5
+    x = (2.0 * torch.randn((beams, V), generator=torch.Generator().manual_seed(4))).to(t)
+    x[0, 8192:32768] = low
+    x[1, 32768:] = low
+    keep = x[2, [3, 20000, 39999]].clone()
+    x[2] = low
+    x[2, [3, 20000, 39999]] = keep
+    x[3] = low
+    scores = torch.tensor([[-1.0, -1.5, -0.5, 6.0, -2.0]])
+    for n_out in (5, 64):
+        got = tg.beam_select(dev(x), dev(scores), n_out)
+        _check_beams(x, scores, n_out, got)
+        assert set(range(5)) >= set(got[1].tolist()[0]) and 2 in got[1].tolist()[0]
+    alone = tg.beam_select(dev(x[3:4].clone()), torch.zeros((1, 1), device="cuda"), 3)
+    assert alone[2].tolist() == [[0, 1, 2]]
+    assert_close("even", alone[0].cpu().numpy(), np.full((1, 3), -np.log(V)), 1e-6, 2.0 ** -23)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_beam_select_largest_values(dtype):
+    """A logit of 3e38: no other token has a weight, and all have finite scores."""
+    t = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    V = 20000
+    x = (2.0 * torch.randn((2, V), generator=torch.Generator().manual_seed(5))).to(t)
+    x[0, 17000] = 3e38
+    x[1, 100:20000] = -1e38
+    scores = torch.tensor([[-3.0, -1.0]])
+    got = tg.beam_select(dev(x), dev(scores), 4)
+    _check_beams(x, scores, 4, got)
+    assert 17000 in got[2].tolist()[0]
