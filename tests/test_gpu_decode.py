@@ -429,6 +429,20 @@ def test_cache_compact_matches_oracle(B, page, P, longest):
     assert torch.equal(again.refs, rf)
 
 
+@pytest.mark.parametrize("B,P", [(64, 4096), (65, 4096), (64, 4097), (1, 4097), (1024, 3000), (3, 65536)])
+def test_cache_compact_on_a_cluster(B, P):
+    """Both sides of the sizes from which a cluster of CTAs renumbers, many times in a row: every launch's
+    CTAs must all run before one writes another's shared memory."""
+    rng = np.random.default_rng(B + P)
+    table, lens, refs = _random_cache(rng, B, 16, P, 16 * (P // B) // 2, P // B)
+    want = do.cache_compact(table, lens, refs, 16)
+    t, ln, rf = _i32(table), _i32(lens), _i32(refs)
+    _check_update(tg.cache_compact(t, ln, rf, 16), want)
+    got = [tg.cache_compact(t, ln, rf, 16) for _ in range(50)]
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, got[0]))
+    _check_update(got[-1], want)
+
+
 @pytest.mark.parametrize("shape,dtype", [((3, 40, 2, 16, 64), torch.bfloat16), ((1, 40, 16), torch.float32),
                                          ((2, 40, 8, 64, 128), torch.float32), ((1, 40, 5, 48), torch.uint8)])
 def test_cache_copy_pages(shape, dtype):
