@@ -292,6 +292,13 @@ class PagedCache:
         return c.counts
 
 
+def _forked(pos, parent):
+    """Every sequence's position after a fork.  One without a parent (-1; or a number outside the batch,
+    which the cache's kernels skip and report) is empty and starts again at position 0."""
+    there = (parent >= 0) & (parent < pos.shape[0])
+    return torch.where(there, pos[parent.clamp(0, pos.shape[0] - 1).long()], 0)
+
+
 class GatedDecoder:
     """Decodes through a GatedStack's layers from the cache its prefill emits.
 
@@ -345,8 +352,7 @@ class GatedDecoder:
                              f"{(self.batch, ly.shape[1])} {ly.dtype}")
         self.cache.grow(parent=parent)
         if parent is not None:
-            # (a freed sequence, parent -1, starts again at position 0)
-            self.pos.copy_(torch.where(parent >= 0, self.pos[parent.clamp(min=0).long()], 0))
+            self.pos.copy_(_forked(self.pos, parent))
         for i, ly in enumerate(st.layers):
             a = rmsnorm(x, ly["w_ln1"], st.eps)
             qkv = torch.mm(a, ly["wqkv"].t())

@@ -318,3 +318,17 @@ def test_binding_rejects_mismatched_operands():
     _raises("logits: shape", tg.beam_select, x[:5], s)
     _raises("scores: dtype", tg.beam_select, x, s.double())
     _raises("workspace", tg.beam_select, x, s, 2, torch.zeros(4))
+
+
+# ---- the decoder's host side -------------------------------------------------------------------
+
+
+def test_forked_positions_stay_in_range():
+    """Parents outside the batch index nothing: such a sequence starts over, as in the cache."""
+    from learned_token_pruning_gate_b200.pipeline import _forked
+
+    pos = torch.tensor([7, 9, 4], dtype=torch.int32)
+    for parent, want in (([2, 0, 0], [4, 7, 7]), ([-1, 1, -1], [0, 9, 0]), ([3, 2 ** 31 - 1, 2], [0, 0, 4]),
+                         ([-2, -2 ** 31, 1], [0, 0, 9])):
+        got = _forked(pos, torch.tensor(parent, dtype=torch.int32))
+        assert got.tolist() == want and got.dtype == torch.int32

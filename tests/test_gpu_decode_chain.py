@@ -226,3 +226,21 @@ def test_out_of_pages_keeps_the_others():
     cache.grow(dev(torch.tensor([0, 0, 1], dtype=torch.int32)))
     assert cache.start.tolist() == [0, 16] and cache.lens.tolist() == [0, 17]
     assert tg.device_status() == 0
+
+
+def test_step_with_parents_outside_the_batch():
+    """Parents that no sequence has: bit 64 of the status, those sequences start over, the others go on."""
+    lens = [21, 40]
+    d, cu, pos, x0, ls, layers, fresh = _decoder(lens, 3, 1, 128, 4, 2, 64, 256, "fp32", 16)
+    i32 = lambda *p: dev(torch.tensor(p, dtype=torch.int32))  # noqa: E731
+    d.prefill(dev(x0).clone())
+    d.step(dev(fresh[0]).clone())
+    want = d.pos.tolist()
+    d.step(dev(fresh[1]).clone(), i32(10 ** 6, 1))
+    torch.cuda.synchronize()
+    assert tg.device_status() == 64
+    assert d.cache.lens.tolist() == [1, 42] and d.pos.tolist() == [1, want[1] + 1]
+    d.step(dev(fresh[2]).clone(), i32(0, -7))
+    torch.cuda.synchronize()
+    assert tg.device_status() == 64
+    assert d.cache.lens.tolist() == [2, 1] and d.pos.tolist() == [2, 1]
