@@ -19,7 +19,7 @@
 // logits; the exponentials alone are 2.8 us of the special-function units for 96
 // rows of 131071) and the chain of its barriers, the merge the dependent steps of
 // one CTA per group (log-sums in 64 bits 1.5 us, rankings 1.8 us).  96 rows of
-// 131071 bf16 logits take 16.3 us on the device (HBM floor 3.9), 4 rows of 32000
+// 131071 bf16 logits take 14.9 us on the device (HBM floor 3.9), 4 rows of 32000
 // fp32 7.0 us.  With a chunk's threshold found by comparing every thread's maximum
 // with every other's the chunks took 48 us instead of 12; with a group joined in
 // the CTA that finishes its last chunk, in place of a second launch, the calls
@@ -56,6 +56,9 @@ struct BeamWork {
   float2* sums;
   uint64_t* keys;
 };
+
+__device__ __forceinline__ uint32_t raw_bits(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t raw_bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x); }
 
 // A thread's logits as they come from memory: 16-byte pieces, unpacked where they are used, so
 // that bf16 ones take half the registers.
@@ -113,9 +116,32 @@ struct Logits {
   }
 };
 
+// The 16-byte pieces that hold `kLead` elements of what comes before a lane's tokens, turned into its
+// tokens: each piece's last words and the first of the next, which the next lane has (lane 31's next
+// is lane 0's of the piece after; `behind` for the last).
+template <typename T, int kLead>
+__device__ __forceinline__ void shift_pieces(Logits<T>& x, const uint32_t (&behind)[4]) {
+  constexpr int kBytes = kLead * static_cast<int>(sizeof(T)), kWord = kBytes / 4;
+  constexpr bool kSplit = kBytes % 4 != 0;  // tokens straddle words
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t w[8];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      w[n] = x.w[4 * i + n];
+      const uint32_t next = i < 7 ? x.w[4 * (i + 1 < 8 ? i + 1 : 7) + n] : behind[n];
+      w[4 + n] = n < kWord + kSplit ? __shfl_sync(0xffffffffu, lane == 0 ? next : w[n], (lane + 1) & 31) : 0u;
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      x.w[4 * i + n] = kSplit ? __funnelshift_r(w[n + kWord], w[n + kWord + 1 < 8 ? n + kWord + 1 : 7], 16) : w[n + kWord];
+  }
+}
+
 template <typename T>
 __host__ __device__ inline int chunks_of(int vocab) {
-  return (vocab + 16 / static_cast<int>(sizeof(T)) - 1 + kChunk<T> - 1) / kChunk<T>;
+  return (vocab + kChunk<T> - 1) / kChunk<T>;
 }
 
 // Larger logit first, then the lower token; 0 for what is no candidate.
@@ -131,7 +157,7 @@ constexpr uint32_t kLowestKey = 0x00800000u;  // order_key of the lowest finite 
 
 template <typename T>
 __global__ void __launch_bounds__(kChunkThreads, 4)
-    beam_chunk_kernel(const T* __restrict__ logits, int vocab, int n_out, int chunks, BeamWork ws) {
+    beam_chunk_kernel(const T* __restrict__ logits, int rows, int vocab, int n_out, int chunks, BeamWork ws) {
   using L = Logits<T>;
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
   constexpr int kWarps = kChunkThreads / 32;
@@ -146,31 +172,72 @@ __global__ void __launch_bounds__(kChunkThreads, 4)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / chunks;
   const int chunk = static_cast<int>(blockIdx.x - row * chunks);
-  // A row may start anywhere: its 16-byte pieces begin at the boundary at or before it, `lead` tokens early.
+  // Which tokens a thread has does not depend on where the row starts, so rows of the same logits
+  // have the same sums to the last bit.  A row may start anywhere: its 16-byte pieces begin at the
+  // boundary at or before a lane's first token, `lead` tokens early, and are then moved by that much.
+  // (With tokens counted from the boundary in place of the move, and a CTA's pieces side by side,
+  // 96 x 131071 bf16 took 16.3 us for 14.9 and 4 x 32000 fp32 6.8 for 7.0.)
   const T* r = logits + row * vocab;
+  const int left = static_cast<int>(min((rows - row) * vocab, int64_t{1} << 30));  // what can be read from here
   const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
-  const int t0 = chunk * kChunk<T> - lead + tid * kVec;  // token of the thread's first element
-  auto token = [&](int e) { return t0 + (e / kVec) * (kChunkThreads * kVec) + e % kVec; };
+  const int t0 = chunk * kChunk<T> + (warp * 8 * 32 + lane) * kVec;  // the thread's first token
+  auto token = [&](int e) { return t0 + (e / kVec) * (32 * kVec) + e % kVec; };
   L x;
+  uint32_t behind[4] = {};
+  auto load = [&](int t, uint32_t* w) {  // (t < 0 lies in the row before: a first row has no lead)
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    if (t < vocab && t + kVec <= left) u = __ldg(reinterpret_cast<const uint4*>(r + t));
+    w[0] = u.x;
+    w[1] = u.y;
+    w[2] = u.z;
+    w[3] = u.w;
+  };
+  auto load_end = [&](int t, uint32_t* w) {  // a piece that reaches past the last row: its tokens one at a time
+    if (t >= vocab || t + kVec <= left) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int t = t0 + i * kChunkThreads * kVec;
-    if (t >= 0 && t + kVec <= vocab) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(r + t));
-      x.w[4 * i] = u.x;
-      x.w[4 * i + 1] = u.y;
-      x.w[4 * i + 2] = u.z;
-      x.w[4 * i + 3] = u.w;
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < kVec / 4; ++e)
+        if (t + n * (kVec / 4) + e < vocab) w[n] |= raw_bits(r[t + n * (kVec / 4) + e]) << (16 * e);
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load(t0 + i * 32 * kVec - lead, &x.w[4 * i]);
+  if (lead != 0 && lane == 0) load(t0 + 8 * 32 * kVec - lead, behind);
+  if (left < vocab + kVec && (chunk + 1) * kChunk<T> + kVec > vocab && (left + lead) % kVec != 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_end(t0 + i * 32 * kVec - lead, &x.w[4 * i]);
+    if (lead != 0 && lane == 0) load_end(t0 + 8 * 32 * kVec - lead, behind);
+  }
+  if (lead != 0) {
+    if constexpr (L::kHalf) {
+      switch (lead) {
+        case 1: shift_pieces<T, 1>(x, behind); break;
+        case 2: shift_pieces<T, 2>(x, behind); break;
+        case 3: shift_pieces<T, 3>(x, behind); break;
+        case 4: shift_pieces<T, 4>(x, behind); break;
+        case 5: shift_pieces<T, 5>(x, behind); break;
+        case 6: shift_pieces<T, 6>(x, behind); break;
+        default: shift_pieces<T, 7>(x, behind);
+      }
     } else {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e)
-        x.set(i * kVec + e, t + e >= 0 && t + e < vocab ? static_cast<float>(r[t + e]) : -INFINITY);
+      switch (lead) {
+        case 1: shift_pieces<T, 1>(x, behind); break;
+        case 2: shift_pieces<T, 2>(x, behind); break;
+        default: shift_pieces<T, 3>(x, behind);
+      }
     }
   }
+  if (t0 + 7 * 32 * kVec + kVec > vocab) {  // what lies behind the row
+#pragma unroll
+    for (int e = 0; e < L::kN; ++e)
+      if (token(e) >= vocab) x.set(e, -INFINITY);
+  }
 
-  // the thread's largest logit; the largest and smallest of these in the chunk
+  // the thread's largest logit; the largest and smallest of these in the chunk (the smallest above
+  // -inf: a ragged chunk has threads without tokens)
   const uint32_t key = order_key(x.largest());
-  const uint32_t warp_max = __reduce_max_sync(0xffffffffu, key), warp_min = __reduce_min_sync(0xffffffffu, key);
+  const uint32_t warp_max = __reduce_max_sync(0xffffffffu, key);
+  const uint32_t warp_min = __reduce_min_sync(0xffffffffu, key >= kLowestKey ? key : 0xffffffffu);
   if (lane == 0) {
     red_max[warp] = warp_max;
     red_min[warp] = warp_min;
@@ -248,7 +315,7 @@ __global__ void __launch_bounds__(kChunkThreads, 4)
 #pragma unroll 1
       for (int e = 0; e < L::kN; ++e) {
         const int t = token(e);
-        if (t < 0 || t >= vocab) continue;
+        if (t >= vocab) continue;
         const uint64_t one = logit_key(static_cast<float>(r[t]), t);
         if (one < last && one > k) k = one;
       }
@@ -426,9 +493,9 @@ tg_status launch_beam_select(const void* logits, tg_dtype dt, const float* score
   cudaError_t e =
       dt == TG_BF16
           ? launch_pdl(beam_chunk_kernel<__nv_bfloat16>, grid, dim3(kChunkThreads), 0, st,
-                       static_cast<const __nv_bfloat16*>(logits), vocab, n_out, chunks, ws)
+                       static_cast<const __nv_bfloat16*>(logits), groups * beams, vocab, n_out, chunks, ws)
           : launch_pdl(beam_chunk_kernel<float>, grid, dim3(kChunkThreads), 0, st,
-                       static_cast<const float*>(logits), vocab, n_out, chunks, ws);
+                       static_cast<const float*>(logits), groups * beams, vocab, n_out, chunks, ws);
   if (e != cudaSuccess) return cuda_check(e, "beam chunk launch");
   const size_t per_group = static_cast<size_t>(beams) * chunks;
   const size_t smem = (per_group + n_out * (n_out + 1) / 2 + 2 * kBatch) * (sizeof(uint64_t) + sizeof(uint32_t));

@@ -704,3 +704,35 @@ def test_beam_select_largest_values(dtype):
     got = tg.beam_select(dev(x), dev(scores), 4)
     _check_beams(x, scores, 4, got)
     assert 17000 in got[2].tolist()[0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [33, 1001, 8195, 50257, 131071])
+def test_beam_select_equal_beams_at_odd_vocabularies(V, dtype):
+    """Beams of the same logits and the same score: every token's beams come in their order.  With an odd
+    vocabulary the rows start at every offset from a 16-byte boundary, which the rows' sums may not show."""
+    t = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    beams, n_out = 8, 24
+    for seed in range(4):
+        row = 2.0 * torch.randn((2, 1, V), generator=torch.Generator().manual_seed(100 * V + seed))
+        x = row.expand(2, beams, V).reshape(2 * beams, V).to(t).contiguous()
+        scores = torch.tensor([[-1.25] * beams, [-0.5] * beams])
+        _check_beams(x, scores, n_out, tg.beam_select(dev(x), dev(scores), n_out))
+    flat = torch.full((beams, V), -3.0, dtype=t)
+    _check_beams(flat, scores[:1], n_out, tg.beam_select(dev(flat), dev(scores[:1]), n_out))
+
+
+@pytest.mark.parametrize("dtype,Vs", [("bf16", (16383, 16385, 16386, 16391, 7)), ("fp32", (8191, 8193, 8194, 8195, 3))])
+def test_beam_select_row_ends(dtype, Vs):
+    """Rows that end just before or behind a chunk's end, the last row at every offset from a 16-byte
+    boundary; the first and last tokens, and those at the chunk's end, are the best."""
+    t = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+    for V in Vs:
+        for beams in range(1, 10):
+            x = torch.randn((beams, V), generator=torch.Generator().manual_seed(V + beams)).to(t)
+            marked = sorted({at for at in (0, 1, V // 2 // 8 * 8 - 1, V - 9, V - 8, V - 7, V - 6, V - 5, V - 4, V - 3,
+                                           V - 2, V - 1) if 0 <= at < V})
+            for b in range(beams):
+                x[b, marked] = (6.0 + torch.arange(len(marked)).roll(b) + 0.25 * b).to(t)
+            scores = torch.linspace(-1.0, -0.25, beams)[None]
+            _check_beams(x, scores, 64, tg.beam_select(dev(x), dev(scores), 64))
