@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kChunkThreads = 256;
 constexpr int kMaxOut = 2 * TG_MAX_BEAMS;
+constexpr int kMaxVocab = 1 << 20;  // as the C ABI checks
 // Logits per thread and per CTA: 128 bytes a thread.
 template <typename T>
 constexpr int kPerThread = 128 / static_cast<int>(sizeof(T));
@@ -476,6 +477,11 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 }  // namespace
 
+// Dynamic shared memory of a merge: the heads of the lists and the candidates.
+static size_t merge_smem(int lists, int n_out) {
+  return (static_cast<size_t>(lists) + n_out * (n_out + 1) / 2 + 2 * kBatch) * (sizeof(uint64_t) + sizeof(uint32_t));
+}
+
 size_t beam_select_workspace_bytes(int groups, int beams, int vocab, int n_out) {
   const size_t lists = static_cast<size_t>(groups) * beams * chunks_of<float>(vocab);  // (bf16 takes fewer)
   return (lists * sizeof(float2) + 15) / 16 * 16 + lists * n_out * sizeof(uint64_t);
@@ -497,10 +503,11 @@ tg_status launch_beam_select(const void* logits, tg_dtype dt, const float* score
           : launch_pdl(beam_chunk_kernel<float>, grid, dim3(kChunkThreads), 0, st,
                        static_cast<const float*>(logits), groups * beams, vocab, n_out, chunks, ws);
   if (e != cudaSuccess) return cuda_check(e, "beam chunk launch");
-  const size_t per_group = static_cast<size_t>(beams) * chunks;
-  const size_t smem = (per_group + n_out * (n_out + 1) / 2 + 2 * kBatch) * (sizeof(uint64_t) + sizeof(uint32_t));
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const size_t smem = merge_smem(beams * chunks, n_out);
+  if (smem > 40 * 1024) {  // (48 KB without asking, of which the kernel has some for itself)
+    // always the most that any call needs, so that calls of several host threads set the same
+    e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(merge_smem(TG_MAX_BEAMS * chunks_of<float>(kMaxVocab), kMaxOut)));
     if (e != cudaSuccess) return cuda_check(e, "beam merge shared memory");
   }
   return cuda_check(launch_pdl(beam_merge_kernel, dim3(static_cast<unsigned>(groups)), dim3(kMergeThreads), smem,

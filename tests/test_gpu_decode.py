@@ -14,6 +14,10 @@ Error budgets, per element, u = half a step of the output type (2^-8 bf16, 2^-24
               the state; the output is rounded once (bf16: 2^-8 relative).
   beams       the score's 32-bit storage: 2^-24 relative, plus 1e-6 for the chunk sums.
 Integers and copied bytes are equal."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -736,3 +740,23 @@ def test_beam_select_row_ends(dtype, Vs):
                 x[b, marked] = (6.0 + torch.arange(len(marked)).roll(b) + 0.25 * b).to(t)
             scores = torch.linspace(-1.0, -0.25, beams)[None]
             _check_beams(x, scores, 64, tg.beam_select(dev(x), dev(scores), 64))
+
+
+def test_beam_select_merge_memory():
+    """Sizes whose merge takes just under 48 KB of dynamic shared memory, in a process that has launched
+    no larger one: the kernel's own few hundred bytes count too."""
+    code = """if 1:
+        import torch
+        import learned_token_pruning_gate_b200 as tg
+        g = torch.Generator("cuda").manual_seed(6)
+        for V in (500000, 503000):
+            x = torch.randn((32, V), generator=g, device="cuda") * 2.0
+            scores = -torch.rand((1, 32), generator=g, device="cuda")
+            _, parent, token = tg.beam_select(x, scores, 64)
+            total = (x.double() - torch.logsumexp(x.double(), 1, keepdim=True) + scores.double().T).reshape(-1)
+            assert torch.equal(parent[0].long() * V + token[0], torch.topk(total, 64).indices)
+        print("equal")
+    """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.split() == ["equal"], run.stderr[-2000:]
