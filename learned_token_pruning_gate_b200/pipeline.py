@@ -309,11 +309,18 @@ class GatedDecoder:
     from one another: what beam_select returns, flattened.
 
     beams: sequences per prompt.  Sequence p * beams of prompt p gets the prefill; the first step
-    forks it (parent = p * beams for all of the prompt's beams)."""
+    forks it (parent = p * beams for all of the prompt's beams).
+
+    ValueError when the pages, or a table of max_pages, cannot hold the kept rows.  Room for new
+    tokens is up to the caller: a sequence whose token found none has cache.start = -1 after step()."""
 
     def __init__(self, stack, pages, page_size, max_pages, beams=1):
         self.stack, self.beams = stack, beams
         self.n_prompts = len(stack.ck) - 1
+        need = -(-np.diff(stack.ck).astype(np.int64) // page_size)  # pages of every prompt's kept rows
+        if need.sum() > pages or need.max(initial=0) > max_pages:
+            raise ValueError(f"the kept rows take {need.sum()} pages, {need.max(initial=0)} of one prompt: "
+                             f"more than pages={pages} or max_pages={max_pages}")
         self.batch = self.n_prompts * beams
         dt, dev = stack.cache_k.dtype, stack.cache_k.device
         self.cache = PagedCache(len(stack.layers), pages, stack.Hkv, page_size, stack.dh, self.batch,

@@ -332,3 +332,21 @@ def test_forked_positions_stay_in_range():
                          ([-2, -2 ** 31, 1], [0, 0, 9])):
         got = _forked(pos, torch.tensor(parent, dtype=torch.int32))
         assert got.tolist() == want and got.dtype == torch.int32
+
+
+def test_decoder_refuses_a_cache_too_small_for_its_prefill():
+    """Pages and tables are counted against the kept rows before anything is allocated."""
+    from types import SimpleNamespace
+
+    from learned_token_pruning_gate_b200.pipeline import GatedDecoder
+
+    ck = np.array([0, 33, 33, 49], np.int32)  # pages of 16: 3, 0 and 1
+    stack = SimpleNamespace(ck=ck, cu=4 * ck, layers=[None], Hq=2, Hkv=1, dh=64,
+                            cache_k=torch.zeros((1, 49, 1, 64)))
+    for pages, max_pages in ((3, 3), (4, 2), (0, 0)):
+        with pytest.raises(ValueError, match="take 4 pages, 3 of one prompt"):
+            GatedDecoder(stack, pages, 16, max_pages, beams=2)
+    d = GatedDecoder(stack, 4, 16, 3, beams=2)
+    assert d.cu_prefill.tolist() == [0, 33, 33, 33, 33, 49, 49] and d.cache.k.shape == (1, 4, 1, 16, 64)
+    none = SimpleNamespace(**dict(vars(stack), ck=np.zeros(1, np.int32), cu=np.zeros(1, np.int32)))
+    assert GatedDecoder(none, 1, 16, 1).batch == 0
