@@ -569,6 +569,8 @@ TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int3
  *         must not overlap on the GPU.
  *   head_dim 64 or 128, n_q_heads <= 512, batch * max_pages * page_size <= 2^36;
  *   q, k_pages, v_pages and out 16-byte aligned.
+ *   out may be q; out, lse and the workspace may not overlap each other or an
+ *   input otherwise.
  */
 TG_API tg_status tg_paged_attention(const void* q, const void* k_pages, const void* v_pages,
                                     tg_dtype dtype, int32_t batch, int32_t n_q_heads,

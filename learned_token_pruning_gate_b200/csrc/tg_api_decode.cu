@@ -103,13 +103,25 @@ tg_status tg_paged_attention(const void* q, const void* k_pages, const void* v_p
     return set_error(TG_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
     return set_error(TG_ERR_ALIGNMENT, "q, k_pages, v_pages and out must be 16-byte aligned");
+  size_t need = 0;
   if (workspace) {
-    const size_t need = paged_attention_workspace_bytes(dtype, batch, n_q_heads, n_kv_heads, head_dim);
+    need = paged_attention_workspace_bytes(dtype, batch, n_q_heads, n_kv_heads, head_dim);
     if (workspace_bytes < need)
       return set_error(TG_ERR_WORKSPACE, "paged attention workspace: %zu bytes given, %zu needed",
                        workspace_bytes, need);
     if (!aligned16(workspace)) return set_error(TG_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
   }
+  const size_t rows = static_cast<size_t>(batch) * n_q_heads, esz = dtype == TG_BF16 ? 2 : 4;
+  const size_t tokens = static_cast<size_t>(n_pages) * page_size, pool_bytes = tokens * n_kv_heads * head_dim * esz;
+  const Span in[] = {{q, rows * head_dim * esz, "q"}, {k_pages, pool_bytes, "k_pages"},
+                     {v_pages, pool_bytes, "v_pages"}, {table, 4 * static_cast<size_t>(batch) * max_pages, "table"},
+                     {lens, 4 * static_cast<size_t>(batch), "lens"}, {logsig_pages, 4 * tokens, "logsig_pages"},
+                     {gain, 4 * static_cast<size_t>(n_q_heads), "gain"},
+                     {temp, 4 * static_cast<size_t>(n_q_heads), "temp"}};
+  const Span outs[] = {{out, rows * head_dim * esz, "out"}, {lse, lse ? 4 * rows : 0, "lse"},
+                       {workspace, need, "workspace"}};
+  const int same[] = {0, -1, -1};  // (a unit's query rows are read before its output is written)
+  if ((r = check_spans(in, 8, outs, 3, same)) != TG_OK) return r;
   if ((r = status_word(&a.status)) != TG_OK) return r;
   a.q = q;
   a.k_pages = k_pages;

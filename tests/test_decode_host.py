@@ -350,3 +350,23 @@ def test_decoder_refuses_a_cache_too_small_for_its_prefill():
     assert d.cu_prefill.tolist() == [0, 33, 33, 33, 33, 49, 49] and d.cache.k.shape == (1, 4, 1, 16, 64)
     none = SimpleNamespace(**dict(vars(stack), ck=np.zeros(1, np.int32), cu=np.zeros(1, np.int32)))
     assert GatedDecoder(none, 1, 16, 1).batch == 0
+
+
+def test_paged_attention_refuses_overlap(L):
+    """Outputs and workspace in one another or in an input, but for out == q."""
+    def call(q=_p(0), k=_p(1), v=_p(2), B=2, Hq=4, Hkv=2, d=64, P=8, page=16, table=_p(3), mp=4, lens=_p(4), ls=_p(9),
+             gain=_p(5), temp=_p(6), out=_p(7), lse=_p(8), ws=None, nb=0):
+        return L.tg_paged_attention(q, k, v, 0, B, Hq, Hkv, d, P, page, table, mp, lens, ls, gain, temp, out, lse, ws, nb,
+                                    None)
+    at = lambda n, off: ctypes.c_void_p(_p(n).value + off)  # noqa: E731
+    # (q and out: 1024 bytes; k and v: 32768; table 32, lens 8, log-gates 512, gain and temp 16, lse 32)
+    refused = [dict(out=at(0, 16)), dict(out=at(1, 32752)), dict(out=at(2, 0)), dict(out=at(3, 16)), dict(out=at(4, 0)),
+               dict(out=at(9, 496)), dict(out=at(5, 0)), dict(out=at(6, 0)), dict(out=at(8, 16)), dict(lse=at(0, 1020)),
+               dict(lse=at(1, 4)), dict(lse=at(3, 28)), dict(lse=at(4, 4)), dict(lse=at(9, 508)), dict(lse=at(5, 12)),
+               dict(lse=at(6, 0)), dict(lse=at(7, 1020)), dict(out=_p(0), lse=at(0, 0))]
+    n = ctypes.c_size_t(0)
+    assert L.tg_paged_attention_workspace_bytes(0, 2, 4, 2, 64, ctypes.byref(n)) == OK and n.value > 0
+    refused += [dict(ws=at(i, 0), nb=n.value) for i in range(10)]
+    for kw in refused:
+        assert call(**kw) == INVALID and b"overlap" in L.tg_last_error_message(), kw
+    assert call(B=0, out=at(0, 16)) == OK  # (nothing is read or written)
