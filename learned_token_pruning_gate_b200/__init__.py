@@ -887,9 +887,10 @@ def cache_update(table, lens, refs, page_size, parent=None, cu_new=None, table_o
         lens_out, start, copy_src, copy_dst = small
         _check("tg_cache_update", library().tg_cache_update(
             table.data_ptr(), lens.data_ptr(), B, refs.data_ptr(), P, page_size, mp,
-            _addr(parent), Bo, _addr(cu_new), table_out.data_ptr(), lens_out.data_ptr(),
-            refs_out.data_ptr(), start.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(),
-            _raw_stream(i)))
+            # (an empty list of parents has no address; null would mean that there is none)
+            _addr(parent) if Bo else lens.data_ptr(), Bo, _addr(cu_new), table_out.data_ptr(),
+            lens_out.data_ptr(), refs_out.data_ptr(), start.data_ptr(), copy_src.data_ptr(),
+            copy_dst.data_ptr(), _raw_stream(i)))
     return CacheUpdate(table_out, lens_out, refs_out, start, copy_src, copy_dst)
 
 

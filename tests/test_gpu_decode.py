@@ -760,3 +760,13 @@ def test_beam_select_merge_memory():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and run.stdout.split() == ["equal"], run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("B,P", [(4, 40), (70, 5000)])
+def test_cache_update_to_no_sequences(B, P):
+    """A fork into no sequences (no parents at all, which is not the absence of parents) frees every page."""
+    table, lens, refs = _random_cache(np.random.default_rng(3), B, 16, P, 100, 8)
+    got = tg.cache_update(_i32(table), _i32(lens), _i32(refs), 16, parent=_i32([]))
+    assert refs.any() and not got.refs.any() and got.table.shape == (0, 8) and got.lens.shape == (0,)
+    none = tg.cache_update(got.table, got.lens, got.refs, 16, cu_new=_i32([0]))
+    assert not none.refs.any() and none.start.shape == (0,)
