@@ -557,7 +557,8 @@ TG_API tg_status tg_attention_backward_workspace_bytes(int32_t batch, const int3
  * The new token's own k and v are in the cache already (tg_cache_append).  A
  * token whose log-gate is -inf has no weight, whatever the gain and its k and v;
  * a sequence that no token is left of (n = 0 among them) gets out = 0 and
- * lse = -inf.
+ * lse = -inf.  A product gain[h] * logsig[j] beyond fp32 counts as the nearest
+ * finite number, so tokens that a mask's lowest value leaves alone weigh the same.
  *   q     device [batch, n_q_heads, head_dim];  out the same shape and dtype
  *   logsig_pages may be NULL (no bias); gain, temp device [n_q_heads] fp32
  *   lse   device [n_q_heads, batch] fp32 or NULL

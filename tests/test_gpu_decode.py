@@ -770,3 +770,26 @@ def test_cache_update_to_no_sequences(B, P):
     assert refs.any() and not got.refs.any() and got.table.shape == (0, 8) and got.lens.shape == (0,)
     none = tg.cache_update(got.table, got.lens, got.refs, 16, cu_new=_i32([0]))
     assert not none.refs.any() and none.start.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("gain", [1.5, 64.0, -2.0])
+def test_attention_gates_whose_bias_overflows(dtype, gain):
+    """gain x the lowest gate is beyond fp32 where the formula's softmax is not: such tokens alone share
+    their weight evenly; beside others they have none (all of it, under a negative gain)."""
+    p = gen.paged_inputs([40, 300], 4, 2, 64, 16, 9, dtype)
+    p["gain"][:] = gain
+    low = torch.finfo(torch.float32).min
+    ls, t = p["logsig_pages"], p["table"]
+    ls[t[0, :3].long()] = low
+    for j in range(0, 300, 3):
+        ls[int(t[1, j // 16]), j % 16] = low
+    for q in (p, _wide(p)):
+        for workspace in ("auto", None):
+            out, lse = _attend(q, workspace)
+            h = {n: host_f32(x) if x.is_floating_point() else x.numpy() for n, x in q.items()}
+            ref, _, mag = do.paged_attention(*[h[n] for n in ("q", "k_pages", "v_pages", "table", "lens", "logsig_pages",
+                                                              "gain", "temp")])
+            bound = 3e-4 * mag + 1e-6 + (2.0 ** -8 * (np.abs(ref) + mag) if dtype == "bf16" else 0.0)
+            assert (np.abs(host_f32(out) - ref) <= bound).all()
+            assert bool(torch.isfinite(lse).all())  # (of the lowest value's size: no fp32 number is the formula's)
