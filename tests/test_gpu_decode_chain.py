@@ -244,3 +244,35 @@ def test_step_with_parents_outside_the_batch():
     torch.cuda.synchronize()
     assert tg.device_status() == 64
     assert d.cache.lens.tolist() == [2, 1] and d.pos.tolist() == [2, 1]
+
+
+def test_replayed_steps_after_an_odd_number_of_forks():
+    """A step captured once is replayed behind later prefills and forks, however many: the same as eager."""
+    lens, new, beams = [21, 40], 4, 2
+    d, cu, pos, x0, ls, layers, fresh = _decoder(lens, new, 1, 128, 4, 2, 64, 256, "fp32", 16, beams=beams)
+    e, *_ = _decoder(lens, new, 1, 128, 4, 2, 64, 256, "fp32", 16, beams=beams)
+    fork = dev(torch.tensor([0, 0, 2, 2], dtype=torch.int32))
+    swap = dev(torch.tensor([1, 0, 3, 3], dtype=torch.int32))
+    d.prefill(dev(x0).clone())
+    x = dev(fresh[0]).clone()
+    d.step(x)  # (its buffers are allocated)
+    graph, forked = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        d.step(x)
+    with torch.cuda.graph(forked):
+        d.step(x, swap)
+    for turn in range(3):
+        x1 = dev(x0) * (1.0 + turn)
+        d.prefill(x1.clone())
+        e.prefill(x1.clone())
+        for t, (g, parent) in enumerate(((None, fork), (graph, None), (forked, swap), (graph, None))):
+            x.copy_(dev(fresh[t]))
+            if g is None:
+                d.step(x, parent)
+            else:
+                g.replay()
+            want = e.step(dev(fresh[t]).clone(), parent)
+            assert_close(f"prefill {turn} step {t}", host_f32(x), host_f32(want), 1e-6, 1e-6)
+            assert torch.equal(d.cache.lens, e.cache.lens) and torch.equal(d.cache.refs, e.cache.refs)
+    assert tg.device_status() == 0
