@@ -793,3 +793,34 @@ def test_attention_gates_whose_bias_overflows(dtype, gain):
             bound = 3e-4 * mag + 1e-6 + (2.0 ** -8 * (np.abs(ref) + mag) if dtype == "bf16" else 0.0)
             assert (np.abs(host_f32(out) - ref) <= bound).all()
             assert bool(torch.isfinite(lse).all())  # (of the lowest value's size: no fp32 number is the formula's)
+
+
+def test_attention_weights_keep_their_bits():
+    """What is left when all but the last bits of a weight cancel.  Of three tokens two weigh 1 and have
+    v = -hi and -lo, the first 16 bits of the third's weight w, as two bf16 numbers, and the third has v = 1:
+    out = (w - hi - lo) / (2 + w), about 2^-19.5.  q = 0, so logits are gain x gate to half a place.
+    The numerator may be off by w's errors (ex2.approx 2^-22, its argument below 1 rounded twice, 2^-23 in
+    all) and three fp32 additions of sums below 1, truncated: 2^-22 + 2^-23 + 3 x 2^-23 < 8e-7; the weights'
+    first 16 bits alone would be off by 3.8e-6 here."""
+    H, d, page = 8, 64, 16
+    bf = lambda x: torch.tensor(x).to(torch.bfloat16).double().numpy()  # noqa: E731
+    gain = np.random.default_rng(1).uniform(0.05, 0.6, 200000).astype(np.float32)
+    w = np.exp(-gain.astype(np.float64))
+    hi = bf(w)
+    lo = bf(w - hi)
+    best = np.argsort(-np.abs(w - hi - lo))[:H]
+    gain, w, hi, lo = gain[best], w[best], hi[best], lo[best]
+    assert (np.abs(w - hi - lo) > 3.8e-6).all()
+    p = gen.paged_inputs([3], H, H, d, page, 1, "bf16", fill=0.0)
+    at = int(p["table"][0, 0])
+    p["q"].zero_()
+    p["gain"], p["temp"] = torch.from_numpy(gain), torch.ones(H)
+    p["logsig_pages"][at, :3] = torch.tensor([0.0, 0.0, -1.0])
+    for h in range(H):
+        for j, x in enumerate((-hi[h], -lo[h], 1.0)):
+            p["v_pages"][at, h, j] = float(x)
+    want = ((w - hi - lo) / (2.0 + w))[:, None]
+    for q in (p, _wide(p)):
+        for workspace in ("auto", None):
+            out, _ = _attend(q, workspace)
+            assert (np.abs(host_f32(out)[0] - want) <= 8e-7 / (2.0 + w[:, None]) + 2.0 ** -9 * np.abs(want)).all()
