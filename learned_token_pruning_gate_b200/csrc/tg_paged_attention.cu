@@ -1,9 +1,10 @@
 // Gated attention of one new token per sequence over a paged cache:
 //   logit_j = q . k_j / (sqrt(d) tau_h) + g_h l_j,   out = softmax(logit) v
 //
-// Every cached row is read once and used by the few query heads that share it, so
-// the call is bound by HBM (2 flop per byte and query head of a group), and what
-// matters is that all SMs read all the time, whatever the lengths.
+// Every cached row is read once for the query heads that share it, up to 16 of them
+// in bf16 and 4 in fp32 (more read it once per 16 or 4), so the call is bound by HBM
+// (2 flop per byte and query head of a group), and what matters is that all SMs read
+// all the time, whatever the lengths.
 //
 // Work: a unit is (sequence, kv head, block of its query heads), cut into tiles of
 // 64 keys (128 of bf16 rows of 64 columns).  The tiles of all units form one list,
@@ -36,11 +37,14 @@
 // fp32: the same schedule on the CUDA cores, eight lanes to a key.
 //
 // Measured on the device, bf16, 16 query heads over 8 kv heads of 128: 7 sequences
-// of 1151 to 131073 tokens 138 us (99% of the copy rate), 16 of 2304 to 2817 33 us
-// (77%).  About 5 us of a call on the list are latency: lengths, table and first
+// of 1151 to 131073 tokens, 227488 in all, 145 us (99% of the copy rate), 16 of 2304
+// to 2817 33.6 us (77%).  About 5 us of a call on the list are latency: lengths, table and first
 // rows one after another (2.5 us), the last sums and the join; 3 us of one on
-// clusters.  32 query
-// heads over 4 of 64, 61 sequences of up to 4353 tokens: 31.2 us (65%).
+// clusters.  32 query heads over 4 of 64, 61 sequences of up to 4353 tokens, 131423 in
+// all: 30.6 us (68%).  32 sequences of 2500 tokens with one kv head of 128: 15.8 us for
+// 16 query heads (40%: 32 units on clusters of eight, two CTAs an SM of 255 registers),
+// 29.7 for 32, which read the rows twice.  fp32, 18 sequences of 2002 tokens, 4 kv heads
+// of 128: 27.6 us for 4 or 8 query heads (83%), 32.0 for 16, 49 for 32.
 //
 // Maxima move lazily: a warp keeps its reference maximum until a logit exceeds it
 // by more than 8, so that weights stay below e^8 and the accumulators are rarely
@@ -153,8 +157,8 @@ __device__ __forceinline__ Keys locate(const Plan& p, int b, int hk, int len, in
 // of three bf16 numbers (the weight rounded, what that cut off, and what is left of it), which hold
 // all 24 bits of a weight, so that the output is a 32-bit evaluation's, rounded once.  With two of
 // them 0.2% of the outputs of 16 x 2500 tokens were rounded to the other neighbour, in place of
-// 0.05%; the third costs 1% of the time there, 2% of 61 sequences of 32/4 heads of 64 and up to 6%
-// with 16 heads to a kv head.
+// 0.05%; the third costs 1% of the time there, 2 to 4% of 61 sequences of 32/4 heads of 64 and up
+// to 6% with 16 heads to a kv head.
 template <int D, int NT>
 struct CoreBf16 {
   static constexpr int kHeads = 8 * NT;
